@@ -19,11 +19,12 @@ LIB_PATH = os.path.join(_HERE, "libssa.so")
  SSA_ERR_BAD_INPUT) = range(7)
 SSA_DT_BF16, SSA_DT_FP32 = 0, 1
 (SSA_OP_SPARSE_FWD, SSA_OP_SPARSE_BWD, SSA_OP_FULL_FWD, SSA_OP_FULL_BWD, SSA_OP_ALIGN_FWD, SSA_OP_SPARSE_INDEX,
- SSA_OP_DECODE) = range(7)
+ SSA_OP_DECODE, SSA_OP_CACHE_DECODE, SSA_OP_CACHE_EVICT) = range(9)
 SSA_SEL_FORCE_CURRENT = 1
 SSA_ACC_OF, SSA_ACC_OS = 1, 2
 SSA_ALIGN_SMOOTH_L1, SSA_ALIGN_L2 = 0, 1
 SSA_BWD_ACCUMULATE, SSA_BWD_GRAD_FP32 = 1, 2
+SSA_ROPE_TRANSPOSE, SSA_ROPE_INTERLEAVED, SSA_ROPE_OWN_LADDER = 1, 2, 4
 SSA_NOALLOC_SCRATCH_BYTES = 32 << 20
 
 # Every entry point include/ssa.h declares.
@@ -33,6 +34,7 @@ EXPORTS = (
     "ssa_full_attn_fwd", "ssa_full_attn_bwd", "ssa_align_loss_fwd", "ssa_align_loss_bwd", "ssa_dropped_mass",
     "ssa_get_device_error", "ssa_status_string", "ssa_full_attn_bwd_noalloc", "ssa_wait_probe",
     "ssa_sparse_decode", "ssa_rope",
+    "ssa_rope_axes", "ssa_cache_append", "ssa_cache_decode", "ssa_cache_evict",
 )
 
 
@@ -92,6 +94,10 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "ssa_wait_probe": (I, [ctypes.c_uint64, P]),
         "ssa_sparse_decode": (I, [C, P, P, P, P, P, P, P, P, P, S, P]),
         "ssa_rope": (I, [C, P, I, I, F, F, I, P]),
+        "ssa_rope_axes": (I, [C, P, I, P, U, F, F, P, P, P, P, P, P, P, P, P]),
+        "ssa_cache_append": (I, [C, I, P, P, P, P, P, P, P, P, P, P, P, P]),
+        "ssa_cache_decode": (I, [C, P, P, P, P, P, P, P, P, P, P, P, P, P, S, P]),
+        "ssa_cache_evict": (I, [C, I, I, I, P, P, P, P, P, P, P, P, P, P, P, S, P]),
         "ssa_status_string": (ctypes.c_char_p, [I]),
     }
     for name, (res, args) in sig.items():
@@ -211,6 +217,48 @@ def ssa_sparse_decode(dims, cache_len, q, Kcache, Vcache, Kbar_cache, idx, o, ls
 def ssa_rope(dims, X, heads, pos0=0, base=10000.0, factor=1.0, transpose=0, stream=None):
     _check("ssa_rope", load().ssa_rope(ctypes.byref(dims), _p(X), int(heads), int(pos0), base, factor, int(transpose),
                                        _stream(stream)))
+
+
+def _strides(t):
+    """Element strides (batch, head, token) of a [B, heads, T, d] tensor as the host array that the library reads;
+    None for a contiguous one, a missing one or an address."""
+    if t is None or isinstance(t, int) or t.is_contiguous():
+        return None
+    if t.stride(3) != 1:
+        raise ValueError("the elements of a row must be adjacent (stride %d)" % t.stride(3))
+    return (ctypes.c_int64 * 3)(*t.stride()[:3])
+
+
+def ssa_rope_axes(dims, pos, sections, Q, Qr, K=None, Kr=None, flags=0, base=10000.0, factor=1.0, stream=None):
+    """sections: the pairs of every axis.  Tensors [B, heads, T, d] may be strided views."""
+    n = len(sections)
+    _check("ssa_rope_axes",
+           load().ssa_rope_axes(ctypes.byref(dims), _p(pos), n, (ctypes.c_int32 * n)(*sections), int(flags), base, factor,
+                                _p(Q), _strides(Q), _p(Qr), _strides(Qr), _p(K), _strides(K), _p(Kr), _strides(Kr),
+                                _stream(stream)))
+
+
+def ssa_cache_append(dims, cache_len, K, V, K8, Kscale, V8, Vscale, Kbar=None, n_new=None, stream=None):
+    """K, V [B, Hkv, n, d] may be strided views."""
+    _check("ssa_cache_append",
+           load().ssa_cache_append(ctypes.byref(dims), K.shape[2], _p(cache_len), _p(n_new), _p(K), _strides(K), _p(V),
+                                   _strides(V), _p(K8), _p(Kscale), _p(V8), _p(Vscale), _p(Kbar), _stream(stream)))
+
+
+def ssa_cache_decode(dims, cache_len, q, K8, Kscale, V8, Vscale, Kbar, idx, o, lse, weight_in=None, weight_out=None,
+                     ws=None, stream=None):
+    _check("ssa_cache_decode",
+           load().ssa_cache_decode(ctypes.byref(dims), _p(cache_len), _p(q), _p(K8), _p(Kscale), _p(V8), _p(Vscale),
+                                   _p(Kbar), _p(idx), _p(o), _p(lse), _p(weight_in), _p(weight_out), _p(ws), _nbytes(ws),
+                                   _stream(stream)))
+
+
+def ssa_cache_evict(dims, keep, cache_len, weight_in, K8, Kscale, V8, Vscale, kept, Kbar=None, weight_out=None,
+                    new_len=None, sink=0, recent=0, ws=None, stream=None):
+    _check("ssa_cache_evict",
+           load().ssa_cache_evict(ctypes.byref(dims), int(keep), int(sink), int(recent), _p(cache_len), _p(new_len),
+                                  _p(weight_in), _p(weight_out), _p(K8), _p(Kscale), _p(V8), _p(Vscale), _p(Kbar),
+                                  _p(kept), _p(ws), _nbytes(ws), _stream(stream)))
 
 
 def ssa_wait_probe(limit_ns: int, stream=None) -> None:

@@ -1,0 +1,737 @@
+// cache_decode.cuh -- attention of one new token per sequence over the 8-bit
+// cache of cache8.cuh, over all blocks (k = 0) or over the own block and the
+// k - 1 highest-scoring ones before it.
+//
+//   logit_u = scale * q . (Kscale * K8_u),  p = softmax over u <= L,
+//   o = sum_u p_u * (Vscale * V8_u),        lse = log sum_u exp(logit_u)
+// and, on demand, the attention weight of every block, sum_h sum_{u in j} p_hu.
+//
+// Bound by reading the cache: 2 d bytes per key and key head, half of what a
+// bf16 cache costs.  A group of G query heads shares each key, so on CUDA cores
+// the conversions and 4 d G operations per key would take longer than the read
+// from G = 4 on; both products therefore run on the tensor cores on the codes
+// as they are (tcgen05 kind::f8f6f4, nothing is converted or copied), and the
+// other operand is brought to e4m3 without losing its precision, as a sum of
+// terms of 4 significant bits each:
+//   q = 2^e (t0 + t1/16):          8 significant bits (bf16) in two terms,
+//   p = (t0 + t1/16 + t2/256)/256: 12 bits, error <= 2^-13 p + 2^-26.
+// The terms are extra columns (N) of the same product, and its results are put
+// together in fp32; N is small and the tensor cores have time to spare.
+//
+//   cache_select_kernel    one CTA per (sequence, key head): block scores and
+//                          the top k - 1 (top_blocks.cuh).  Scores are summed
+//                          in fp64 and rounded to fp32 once, so which blocks
+//                          are chosen does not depend on the order of summation;
+//   cache_attend_kernel    a fixed grid; every CTA takes an equal share of all
+//                          the tiles of 128 keys of all (sequence, key head)
+//                          pairs, so long and short sequences balance, and
+//                          writes an unnormalised partial output, maximum and
+//                          sum for each pair that it touches;
+//   cache_combine_kernel   one CTA per (sequence, key head): joins the partials
+//                          in a fixed order; block weights from the blocks' own
+//                          maxima and sums.
+// No atomics: results are the same from run to run.
+#pragma once
+
+#include "cache8.cuh"
+#include "device.cuh"
+#include "top_blocks.cuh"
+
+namespace ssa {
+
+constexpr int kCacheMaxGroup = 32;  // query heads per key head
+constexpr int kCacheSms = 148;
+
+// Blocks attended and tiles of 128 keys of one key head whose newest token is at position L.
+__device__ __forceinline__ int cache_slots(int L, int T, int s, int k) {
+    if (L < 0 || L >= T) return 0;
+    const int nblk = L / s + 1;
+    return k > 0 ? min(k, nblk) : nblk;
+}
+__device__ __forceinline__ int cache_tiles(int L, int T, int s, int k) {
+    const int n = cache_slots(L, T, s, k);
+    return s == 128 ? n : (n + 1) >> 1;
+}
+
+// ---------------------------------------------------------------------------
+// Selection
+// ---------------------------------------------------------------------------
+// Shared memory: nb keys.  k >= 1.
+__global__ void __launch_bounds__(kTopThreads) cache_select_kernel(const int32_t *__restrict__ cache_len,
+                                                                   const __nv_bfloat16 *__restrict__ q,
+                                                                   const float *__restrict__ Kbar,
+                                                                   int32_t *__restrict__ idx, int Hk, int G, int T,
+                                                                   int s, int k, int nb) {
+    extern __shared__ uint32_t select_key[];
+    __shared__ TopScratch sc;
+    __shared__ double qs[kCacheD];
+    grid_dependents_launch();
+    const int bh = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int L = __ldg(cache_len + bh / Hk);
+    int32_t *out = idx + static_cast<size_t>(bh) * k;
+    if (L < 0 || L >= T) {
+        for (int i = tid; i < k; i += kTopThreads) out[i] = -1;
+        return;
+    }
+    const int bt = L / s, want = min(k - 1, bt);
+    if (want < bt) {
+        if (want > 0) {
+            if (tid < kCacheD) {
+                double v = 0.0;
+                for (int h = 0; h < G; ++h)
+                    v += static_cast<double>(__bfloat162float(q[(static_cast<size_t>(bh) * G + h) * kCacheD + tid]));
+                qs[tid] = v;
+            }
+            __syncthreads();
+            double q4[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) q4[i] = qs[4 * lane + i];
+            constexpr int R = 8;  // rows in flight per warp
+            const float4 *kb = reinterpret_cast<const float4 *>(Kbar + static_cast<size_t>(bh) * nb * kCacheD) + lane;
+            for (int j0 = R * warp; j0 < bt; j0 += R * (kTopThreads / 32)) {
+                float4 v[R];
+#pragma unroll
+                for (int i = 0; i < R; ++i)
+                    v[i] = j0 + i < bt ? __ldg(kb + static_cast<size_t>(j0 + i) * (kCacheD / 4))
+                                       : make_float4(0.f, 0.f, 0.f, 0.f);
+                double part[R];
+#pragma unroll
+                for (int i = 0; i < R; ++i)
+                    part[i] = fma(q4[0], static_cast<double>(v[i].x),
+                                  fma(q4[1], static_cast<double>(v[i].y),
+                                      fma(q4[2], static_cast<double>(v[i].z), q4[3] * static_cast<double>(v[i].w))));
+                // butterfly: three steps hand each lane the sum of one row over 8 lanes, two more the whole sum
+#pragma unroll
+                for (int off = 16, n = R / 2; n >= 1; off >>= 1, n >>= 1) {
+                    const bool up = (lane & off) != 0;
+#pragma unroll
+                    for (int i = 0; i < n; ++i) {
+                        const double send = up ? part[i] : part[i + n], mine = up ? part[i + n] : part[i];
+                        part[i] = mine + __shfl_xor_sync(0xffffffffu, send, off);
+                    }
+                }
+                part[0] += __shfl_xor_sync(0xffffffffu, part[0], 2);
+                part[0] += __shfl_xor_sync(0xffffffffu, part[0], 1);
+                const int r = ((lane >> 4) & 1) * 4 + ((lane >> 3) & 1) * 2 + ((lane >> 2) & 1);
+                if ((lane & 3) == 0 && j0 + r < bt) select_key[j0 + r] = score_key(static_cast<float>(part[0]));
+            }
+            __syncthreads();
+            top_ascending(select_key, bt, want, out, sc);
+        }
+    } else {
+        for (int i = tid; i < want; i += kTopThreads) out[i] = i;
+    }
+    for (int i = want + tid; i < k; i += kTopThreads) out[i] = i == want ? bt : -1;
+}
+
+// ---------------------------------------------------------------------------
+// Attention
+// ---------------------------------------------------------------------------
+// Workspace: partial outputs, one slot for every (CTA, pair) that can meet (slot = CTA + pair, distinct since
+// either grows along the tiles), their (maximum in log2 units, sum); per query head and attended block the
+// same pair for the block alone.
+__host__ __device__ __forceinline__ size_t cache_partials(size_t ctas, size_t pairs) { return ctas + pairs; }
+
+// Position in the sequence of tiles: pair (b, hk), tile t of its nt.
+struct TilePos {
+    int b, hk, t, nt, L;
+    __device__ __forceinline__ void enter(int b_, const int32_t *cache_len, int B, int T, int s, int k) {
+        for (b = b_; b < B; ++b) {
+            L = __ldg(cache_len + b);
+            nt = cache_tiles(L, T, s, k);
+            if (nt > 0) break;
+        }
+        hk = t = 0;
+    }
+    __device__ __forceinline__ void next(const int32_t *cache_len, int B, int Hk, int T, int s, int k) {
+        if (++t < nt) return;
+        t = 0;
+        if (++hk < Hk) return;
+        enter(b + 1, cache_len, B, T, s, k);
+    }
+};
+
+// Tiles of all sequences (times Hk: of all pairs), counted by one warp.
+__device__ __forceinline__ int64_t cache_total_tiles(const int32_t *cache_len, int B, int Hk, int T, int s, int k,
+                                                     int lane) {
+    int64_t n = 0;
+    for (int b = lane; b < B; b += 32) n += cache_tiles(__ldg(cache_len + b), T, s, k);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+    return n * Hk;
+}
+
+// Tiles of the sequences before b, by one warp.
+__device__ __forceinline__ int64_t cache_tiles_before(const int32_t *cache_len, int b, int T, int s, int k, int lane) {
+    int64_t n = 0;
+    for (int i = lane; i < b; i += 32) n += cache_tiles(__ldg(cache_len + i), T, s, k);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+    return n;
+}
+
+// The pair and tile of global tile g, by one warp.
+__device__ __forceinline__ TilePos cache_locate(const int32_t *cache_len, int64_t g, int B, int Hk, int T, int s, int k,
+                                                int lane) {
+    TilePos p;
+    int64_t before = 0;
+    for (int b0 = 0; b0 < B; b0 += 32) {
+        const int L = b0 + lane < B ? __ldg(cache_len + b0 + lane) : -1;
+        const int nt = cache_tiles(L, T, s, k);
+        int64_t upto = static_cast<int64_t>(nt) * Hk;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += v;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, before + upto > g);
+        if (hit) {
+            const int l = __ffs(hit) - 1;
+            p.b = b0 + l;
+            p.nt = __shfl_sync(0xffffffffu, nt, l);
+            p.L = __shfl_sync(0xffffffffu, L, l);
+            const int64_t start = before + __shfl_sync(0xffffffffu, upto, l) - static_cast<int64_t>(p.nt) * Hk;
+            const int at = static_cast<int>(g - start);
+            p.hk = at / p.nt;
+            p.t = at % p.nt;
+            return p;
+        }
+        before += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    p.b = B;  // not reached: g is below the total
+    p.hk = p.t = p.L = 0;
+    p.nt = 1;
+    return p;
+}
+
+template <int NH>
+struct CacheAttendSmem {
+    static constexpr int kStages = 2;
+    static constexpr int kTile = 128 * kCacheD;                      // 16 KB: keys or values of one tile
+    static constexpr int kNS = 2 * NH;                               // columns of the logits' product
+    static constexpr int kNP = (3 * NH + 15) / 16 * 16;              // columns of the output's product
+    static constexpr int kQ = kStages * 2 * kTile;                   // [kNS][128 B]
+    static constexpr int kP = kQ + kNS * 128;                        // [kNP][128 B]
+    static constexpr int kMax = kP + kNP * 128;                      // [NH][4 warps] fp32
+    static constexpr int kSum = kMax + NH * 16;                      // [NH][4 warps] fp32
+    static constexpr int kHead = kSum + NH * 16;                     // [NH] logit factor, [NH] max, [NH] sum
+    static constexpr int kBar = kHead + 3 * NH * 4;
+    static constexpr int kTotal = kBar + 128 + 1024;                 // + alignment of the dynamic base to 1024 B
+    static constexpr int kTmemO = kNS;                               // first column of the output's product
+    static constexpr int kTmemCols = kNS + kNP <= 64 ? 64 : kNS + kNP <= 128 ? 128 : 256;
+};
+
+// Tile of 128 keys (one block of 128 or two of 64):
+//   S^T [128 keys x 2 NH] = K8 . (q terms)^T      A: keys as loaded (K-major), thread = key
+//   weights of the thread's key against the running maxima, split into three terms
+//   O^T [128 dims x 3 NH] = V8^T . (p terms)^T    A: values as loaded (M-major), thread = dim
+// The running maxima and the outputs stay in registers; only O^T of one tile is in tensor memory.
+template <int NH>
+__global__ void __launch_bounds__(128) cache_attend_kernel(
+    const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
+    const int32_t *__restrict__ cache_len, const __nv_bfloat16 *__restrict__ q, const float *__restrict__ Kscale,
+    const float *__restrict__ Vscale, const int32_t *idx, float *__restrict__ opart, float2 *__restrict__ mlpart,
+    float2 *__restrict__ block_ml, int B, int Hk, int G, int T, int s, int k, int nb, float scale_log2) {
+    using SM = CacheAttendSmem<NH>;
+    extern __shared__ __align__(1024) uint8_t cad_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(cad_raw) + 1023) & ~uintptr_t(1023));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t sQ = smem_u32(smem + SM::kQ), sP = smem_u32(smem + SM::kP);
+    float *red_m = reinterpret_cast<float *>(smem + SM::kMax), *red_l = reinterpret_cast<float *>(smem + SM::kSum);
+    float *head_f = reinterpret_cast<float *>(smem + SM::kHead), *head_m = head_f + NH, *head_l = head_m + NH;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + SM::kBar);
+    uint64_t *bar_k = bars, *bar_v = bars + 2, *bar_s = bars + 4, *bar_o = bars + 5;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 6);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + 7);
+
+    // this CTA's share of the tiles
+    const int64_t total = cache_total_tiles(cache_len, B, Hk, T, s, k, lane);
+    if (blockIdx.x == 0)
+        for (int b = tid; b < B; b += 128) {
+            const int L = __ldg(cache_len + b);
+            if (L < -1 || L >= T) record_error(ERR_CACHE_INPUT, 0x703);
+        }
+    const int64_t ctas = min(static_cast<int64_t>(gridDim.x), total);
+    if (static_cast<int64_t>(blockIdx.x) >= ctas) {
+        grid_dependency_wait();
+        return;
+    }
+    const int64_t g0 = blockIdx.x * total / ctas;
+    const int n_tiles = static_cast<int>((blockIdx.x + 1) * total / ctas - g0);
+    TilePos cur = cache_locate(cache_len, g0, B, Hk, T, s, k, lane);
+
+    if (tid == 0) {
+        for (int i = 0; i < 6; ++i) mbar_init(bars + i, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, SM::kTmemCols);
+        tmem_relinquish();
+    }
+    for (int e = tid; e < (SM::kNS + SM::kNP) * 8; e += 128)
+        *reinterpret_cast<uint4 *>(smem + SM::kQ + e * 16) = make_uint4(0u, 0u, 0u, 0u);
+    grid_dependency_wait();  // the selection (k > 0) has been written
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    grid_dependents_launch();
+    const uint32_t tmem = *tmem_slot;
+
+    const int per = 128 / s, seg = tid / s;  // blocks of a tile, this key's block among them
+    struct Blocks {
+        int v[2];
+    };
+    // blocks of a tile (-1: none); only positions that cache_locate and next() give are asked for
+    auto blocks_of = [&](const TilePos &p) {
+        Blocks r;
+        const int ns = cache_slots(p.L, T, s, k);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int slot = p.t * per + i;
+            r.v[i] = -1;
+            if (i < per && slot < ns)
+                r.v[i] = k > 0 ? __ldcg(idx + (static_cast<size_t>(p.b) * Hk + p.hk) * k + slot) : slot;
+        }
+        return r;
+    };
+    auto usable = [&](int blk, int L) { return blk >= 0 && blk <= L / s; };
+    // (thread 0) keys or values of one tile into stage st
+    auto load = [&](const CUtensorMap *map, uint64_t *bar, int st, int off, const TilePos &p, const Blocks &r) {
+        uint32_t bytes = 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (usable(r.v[i], p.L)) bytes += s * kCacheD;
+        mbar_arrive_expect_tx(bar + st, bytes);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (usable(r.v[i], p.L))  // (the host keeps B * Hkv * T below 2^31)
+                tma_load_2d(map, bar + st, smem + st * 2 * SM::kTile + off + i * s * kCacheD, 0,
+                            (p.b * Hk + p.hk) * T + r.v[i] * s);
+    };
+    struct Scales {
+        float k, v, vmax;
+    };
+    auto scales_of = [&](const TilePos &p, const Blocks &r) {  // of this thread's key's block
+        const size_t at = (static_cast<size_t>(p.b) * Hk + p.hk) * nb;
+        Scales c{0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (usable(r.v[i], p.L)) {
+                const float v = __ldg(Vscale + at + r.v[i]);
+                c.vmax = fmaxf(c.vmax, v);
+                if (i == seg) c.v = v, c.k = __ldg(Kscale + at + r.v[i]);
+            }
+        return c;
+    };
+
+    Blocks blk = blocks_of(cur), blk1{{-1, -1}}, blk2{{-1, -1}};
+    Scales sc = scales_of(cur, blk), sc1{0.f, 0.f, 0.f};
+    TilePos pos1 = cur, pos2;
+    if (n_tiles > 1) {
+        pos1.next(cache_len, B, Hk, T, s, k);
+        blk1 = blocks_of(pos1);
+    }
+    pos2 = pos1;
+    int loaded_k = 0, loaded_v = 0;  // (thread 0) tiles whose loads have been issued
+    if (tid == 0) {
+        load(&mapK, bar_k, 0, 0, cur, blk);
+        load(&mapV, bar_v, 0, SM::kTile, cur, blk);
+        loaded_k = loaded_v = 1;
+        if (n_tiles > 1) {
+            load(&mapK, bar_k, 1, 0, pos1, blk1);
+            load(&mapV, bar_v, 1, SM::kTile, pos1, blk1);
+            loaded_k = loaded_v = 2;
+        }
+    }
+    int issued_s = 0, issued_o = 0;  // (thread 0) products issued
+    auto leave = [&](bool failed) {
+        if (failed && tid == 0) {  // let the loads and products in flight finish
+            for (int st = 0; st < SM::kStages; ++st) {
+                const int nk = (loaded_k - st + 1) / 2, nv = (loaded_v - st + 1) / 2;  // loads into this stage
+                if (nk > 0) mbar_drain(bar_k + st, (nk - 1) & 1);
+                if (nv > 0) mbar_drain(bar_v + st, (nv - 1) & 1);
+            }
+            if (issued_s) mbar_drain(bar_s, (issued_s - 1) & 1);
+            if (issued_o) mbar_drain(bar_o, (issued_o - 1) & 1);
+        }
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        if (warp == 1) tmem_dealloc(tmem, SM::kTmemCols);
+    };
+
+    float o[NH];
+    int pair = -1;
+    for (int it = 0; it < n_tiles; ++it) {
+        const int st = it & 1, ph = (it >> 1) & 1;
+        const int bh = cur.b * Hk + cur.hk;
+        // the next tile's scales and the one after's blocks arrive during this tile
+        if (it + 1 < n_tiles) sc1 = scales_of(pos1, blk1);
+        if (it + 2 < n_tiles) {
+            pos2.next(cache_len, B, Hk, T, s, k);
+            blk2 = blocks_of(pos2);
+        }
+        if (bh != pair) {  // a new group of query heads: two terms per element, two rows per head
+            pair = bh;
+            for (int h = warp; h < G; h += 4) {
+                const uint2 w = __ldg(reinterpret_cast<const uint2 *>(q + (static_cast<size_t>(bh) * G + h) * kCacheD) + lane);
+                const float x[4] = {__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u),
+                                    __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u)};
+                uint32_t top = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+                top = __reduce_max_sync(0xffffffffu, top);
+                const bool finite = top < 0x7F800000u;
+                const float unit = finite ? e4m3_scale(__uint_as_float(top)) : 1.f, inv = pow2_inverse(unit);
+                uint32_t t0 = 0, t1 = 0;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float a = x[2 * i] * inv, c = x[2 * i + 1] * inv;
+                    const uint16_t hi = pack_e4m3x2(a, c);
+                    const float2 f = unpack_e4m3x2(hi);
+                    t0 |= static_cast<uint32_t>(hi) << (16 * i);
+                    t1 |= static_cast<uint32_t>(pack_e4m3x2((a - f.x) * 16.f, (c - f.y) * 16.f)) << (16 * i);
+                }
+                const int unit16 = lane >> 2, in16 = (lane & 3) * 4, h1 = NH + h;
+                *reinterpret_cast<uint32_t *>(smem + SM::kQ + h * 128 + ((unit16 ^ (h & 7)) << 4) + in16) = t0;
+                *reinterpret_cast<uint32_t *>(smem + SM::kQ + h1 * 128 + ((unit16 ^ (h1 & 7)) << 4) + in16) = t1;
+                if (lane == 0) {
+                    // an infinity or NaN in the query makes the row's results NaN, not large
+                    head_f[h] = finite ? unit * scale_log2 : __int_as_float(0x7FC00000);
+                    head_m[h] = -INFINITY;
+                    head_l[h] = 0.f;
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < NH; ++h) o[h] = 0.f;
+            fence_proxy_async_smem();
+            __syncthreads();
+        }
+        bool ok = true;
+        if (tid == 0) {
+            ok = mbar_wait(bar_k + st, ph, abort_flag, 0x711);
+            if (ok) {
+                tc_fence_after();
+                const uint32_t a = smem_u32(smem + st * 2 * SM::kTile);
+                constexpr uint32_t id = idesc_e4m3(128, SM::kNS, false, false);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_e4m3_ss(tmem, smem_desc_sw128(a + kk * 32, 16), smem_desc_sw128(sQ + kk * 32, 16), id,
+                                kk > 0 ? 1u : 0u);
+                mma_commit(bar_s);
+                ++issued_s;
+            }
+        }
+        ok = ok && mbar_wait(bar_s, it & 1, abort_flag, 0x712);
+        if (__syncthreads_or(!ok)) {
+            leave(true);
+            return;
+        }
+        tc_fence_after();
+        if (tid == 0 && it + 2 < n_tiles) {  // the keys have been read
+            load(&mapK, bar_k, st, 0, pos2, blk2);
+            ++loaded_k;
+        }
+        const int my_blk = seg ? blk.v[1] : blk.v[0];
+        const bool valid = usable(my_blk, cur.L) && my_blk * s + tid % s <= cur.L;
+        float p[NH];
+        {
+            const uint32_t row = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+            if constexpr (NH == 8) {
+                float v[16];
+                tmem_ld16(row, v);
+#pragma unroll
+                for (int h = 0; h < 8; ++h) p[h] = fmaf(v[8 + h], 0.0625f, v[h]);
+            } else if constexpr (NH == 16) {
+                float v[32];
+                tmem_ld32(row, v);
+#pragma unroll
+                for (int h = 0; h < 16; ++h) p[h] = fmaf(v[16 + h], 0.0625f, v[h]);
+            } else {
+                float v[32], w[32];
+                tmem_ld32(row, v);
+                tmem_ld32(row + 32, w);
+#pragma unroll
+                for (int h = 0; h < 32; ++h) p[h] = fmaf(w[h], 0.0625f, v[h]);
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+            if (h < G) {
+                p[h] = valid ? p[h] * (sc.k * head_f[h]) : -INFINITY;
+                float m;
+                asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(p[h]));
+                if (lane == 0) red_m[h * 4 + warp] = m;
+            }
+        }
+        __syncthreads();
+        // weights against the new maximum; the outputs so far are brought to it below
+        float vs = sc.v;
+        const float vtop = sc.vmax;
+        vs = vtop > 0.f ? vs / vtop : 0.f;  // both powers of two
+        float sum[NH], shrink[NH];
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+            sum[h] = 0.f;
+            shrink[h] = 1.f;
+            if (h < G) {
+                const float4 r = *reinterpret_cast<const float4 *>(red_m + h * 4);
+                const float old = head_m[h];
+                float m = fmaxf(fmaxf(fmaxf(r.x, r.y), fmaxf(r.z, r.w)), old);
+                if (m == -INFINITY) m = 0.f;  // only overflowing logits: weights 0
+                if (m != old) shrink[h] = fast_exp2(old - m);
+                p[h] = valid ? fast_exp2(p[h] - m) : 0.f;
+                sum[h] = p[h];
+                p[h] *= 256.f * vs;
+            }
+        }
+        // sums over the warp: each step hands a lane half of the heads it holds
+        {
+            int n = NH / 2, off = 16;
+#pragma unroll
+            for (; n >= 1; n >>= 1, off >>= 1) {
+                const bool up = (lane & off) != 0;
+#pragma unroll
+                for (int i = 0; i < NH / 2; ++i) {
+                    if (i < n) {
+                        const float send = up ? sum[i] : sum[i + n], mine = up ? sum[i + n] : sum[i];
+                        sum[i] = mine + __shfl_xor_sync(0xffffffffu, send, off);
+                    }
+                }
+            }
+#pragma unroll
+            for (; off >= 1; off >>= 1) sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], off);
+            constexpr int kLanes = 32 / NH;  // lanes that end up with the same head
+            const int h = lane / kLanes;
+            if (lane % kLanes == 0 && h < G) red_l[h * 4 + warp] = sum[0];
+        }
+        // three terms of every weight into the K-major operand: row term * NH + h, byte = key
+        {
+            uint8_t *base = smem + SM::kP + (tid & 15);
+            const int u16 = tid >> 4;
+            auto put = [&](int row, uint32_t byte) {
+                base[row * 128 + ((u16 ^ (row & 7)) << 4)] = static_cast<uint8_t>(byte);
+            };
+#pragma unroll
+            for (int h = 0; h < NH; h += 2) {
+                if (h < G) {
+                    float a = p[h], c = p[h + 1];
+#pragma unroll
+                    for (int term = 0; term < 3; ++term) {
+                        const uint16_t w = pack_e4m3x2(a, c);
+                        put(term * NH + h, w & 0xFFu);
+                        put(term * NH + h + 1, w >> 8);
+                        const float2 f = unpack_e4m3x2(w);
+                        a = (a - f.x) * 16.f;
+                        c = (c - f.y) * 16.f;
+                    }
+                }
+            }
+        }
+        ok = mbar_wait(bar_v + st, ph, abort_flag, 0x713);
+        if (ok && !valid) {  // whatever the cache holds behind the newest token must not meet even a weight of 0
+            uint4 *row = reinterpret_cast<uint4 *>(smem + st * 2 * SM::kTile + SM::kTile + tid * kCacheD);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) row[i] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        if (__syncthreads_or(!ok)) {
+            leave(true);
+            return;
+        }
+        if (tid == 0) {
+            tc_fence_after();
+            const uint32_t a = smem_u32(smem + st * 2 * SM::kTile + SM::kTile);
+            constexpr uint32_t id = idesc_e4m3(128, SM::kNP, true, false);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+                mma_e4m3_ss(tmem + SM::kTmemO, smem_desc_sw128(a + kk * 4096, 16), smem_desc_sw128(sP + kk * 32, 16),
+                            id, kk > 0 ? 1u : 0u);
+            mma_commit(bar_o);
+            ++issued_o;
+        }
+        // meanwhile: the head's running maximum and sum, and the blocks' own
+        if (tid < G) {
+            const float4 rm = *reinterpret_cast<const float4 *>(red_m + tid * 4);
+            const float4 rl = *reinterpret_cast<const float4 *>(red_l + tid * 4);
+            const float old = head_m[tid];
+            float m = fmaxf(fmaxf(fmaxf(rm.x, rm.y), fmaxf(rm.z, rm.w)), old);
+            if (m == -INFINITY) m = 0.f;
+            const float l = (rl.x + rl.y) + (rl.z + rl.w);
+            head_l[tid] = head_l[tid] * (m != old ? fast_exp2(old - m) : 1.f) + l;
+            head_m[tid] = m;
+            if (block_ml) {
+                const size_t at = (static_cast<size_t>(bh) * G + tid) * (k > 0 ? k : nb) + cur.t * per;
+                if (s == 128) {
+                    block_ml[at] = make_float2(m, l);
+                } else {
+                    block_ml[at] = make_float2(m, rl.x + rl.y);
+                    if (blk.v[1] >= 0) block_ml[at + 1] = make_float2(m, rl.z + rl.w);
+                }
+            }
+        }
+        ok = mbar_wait(bar_o, it & 1, abort_flag, 0x714);
+        if (__syncthreads_or(!ok)) {
+            leave(true);
+            return;
+        }
+        tc_fence_after();
+        if (tid == 0 && it + 2 < n_tiles) {  // the values have been read
+            load(&mapV, bar_v, st, SM::kTile, pos2, blk2);
+            ++loaded_v;
+        }
+        {
+            const uint32_t row = tmem + SM::kTmemO + (static_cast<uint32_t>(warp * 32) << 16);
+            const float unit = vtop * (1.f / 256.f);
+            if constexpr (NH == 8) {
+                float v[32];
+                tmem_ld32(row, v);
+#pragma unroll
+                for (int h = 0; h < 8; ++h)
+                    o[h] = fmaf(fmaf(fmaf(v[16 + h], 0.0625f, v[8 + h]), 0.0625f, v[h]), unit, o[h] * shrink[h]);
+            } else if constexpr (NH == 16) {
+                float v[32], w[16];
+                tmem_ld32(row, v);
+                tmem_ld16(row + 32, w);
+#pragma unroll
+                for (int h = 0; h < 16; ++h)
+                    o[h] = fmaf(fmaf(fmaf(w[h], 0.0625f, v[16 + h]), 0.0625f, v[h]), unit, o[h] * shrink[h]);
+            } else {
+                float v[32];
+#pragma unroll
+                for (int h = 0; h < 32; ++h) o[h] *= shrink[h];
+                float f = unit;
+#pragma unroll
+                for (int term = 0; term < 3; ++term, f *= 0.0625f) {
+                    tmem_ld32(row + 32 * term, v);
+#pragma unroll
+                    for (int h = 0; h < 32; ++h) o[h] = fmaf(v[h], f, o[h]);
+                }
+            }
+            tc_fence_before();
+        }
+        const bool last = it + 1 == n_tiles || pos1.b * Hk + pos1.hk != bh;
+        if (last) {
+            const size_t slot = static_cast<size_t>(blockIdx.x) + bh;
+            float *to = opart + slot * G * kCacheD + tid;
+#pragma unroll
+            for (int h = 0; h < NH; ++h)
+                if (h < G) to[h * kCacheD] = o[h];
+            if (tid < G) mlpart[slot * G + tid] = make_float2(head_m[tid], head_l[tid]);
+            __syncthreads();  // head_* are set anew for the next pair
+        }
+        cur = pos1;
+        pos1 = pos2;
+        blk = blk1;
+        blk1 = blk2;
+        sc = sc1;
+    }
+    leave(false);
+}
+
+// ---------------------------------------------------------------------------
+// Joining the partials: M = max m_i, o = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i, in the order of the CTAs.
+// ---------------------------------------------------------------------------
+__global__ void __launch_bounds__(256) cache_combine_kernel(const int32_t *__restrict__ cache_len,
+                                                            const float *opart, const float2 *mlpart,
+                                                            const float2 *block_ml, const int32_t *idx,
+                                                            __nv_bfloat16 *__restrict__ o, float *__restrict__ lse,
+                                                            const float *weight_in, float *weight_out, int B, int Hk,
+                                                            int G, int T, int s, int k, int nb, int grid) {
+    __shared__ float head_m[kCacheMaxGroup], head_l[kCacheMaxGroup];
+    __shared__ float4 part[8][32];
+    const int bh = blockIdx.x, b = bh / Hk, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int L = __ldg(cache_len + b), nt = cache_tiles(L, T, s, k), ns = cache_slots(L, T, s, k);
+    const int64_t total = cache_total_tiles(cache_len, B, Hk, T, s, k, lane);
+    const int64_t first = cache_tiles_before(cache_len, b, T, s, k, lane) * Hk + static_cast<int64_t>(bh % Hk) * nt;
+    grid_dependency_wait();
+    if (nt == 0) {  // no token (or a bad length): empty attention
+        for (int e = tid; e < G * kCacheD; e += 256) o[static_cast<size_t>(bh) * G * kCacheD + e] = __float2bfloat16_rn(0.f);
+        if (tid < G) lse[static_cast<size_t>(bh) * G + tid] = -INFINITY;
+        if (weight_out)
+            for (int j = tid; j < nb; j += 256)
+                weight_out[static_cast<size_t>(bh) * nb + j] = weight_in ? weight_in[static_cast<size_t>(bh) * nb + j] : 0.f;
+        return;
+    }
+    // CTAs c with tiles of this pair: c * total / ctas <= tile < (c + 1) * total / ctas
+    const int64_t ctas = min(static_cast<int64_t>(grid), total);
+    const int c0 = static_cast<int>(((first + 1) * ctas - 1) / total);
+    const int c1 = static_cast<int>(((first + nt) * ctas - 1) / total);
+    const int np = c1 - c0 + 1;
+    const size_t slot0 = static_cast<size_t>(c0) + bh;
+    const float2 *ml = mlpart + slot0 * G;
+    for (int h = warp; h < G; h += 8) {
+        float m = -INFINITY, l = 0.f;
+        for (int i = lane; i < np; i += 32) m = fmaxf(m, __ldcg(ml + static_cast<size_t>(i) * G + h).x);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+        for (int i = lane; i < np; i += 32) {
+            const float2 a = __ldcg(ml + static_cast<size_t>(i) * G + h);
+            l += a.y * fast_exp2(a.x - m);
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+        if (lane == 0) {
+            head_m[h] = m;
+            head_l[h] = l;
+            lse[static_cast<size_t>(bh) * G + h] = fmaf(m, kLn2, logf(l));
+        }
+    }
+    __syncthreads();
+    // outputs: a warp per head (G >= 8), or several warps per head that take every ng-th partial
+    const int ng = G >= 8 ? 1 : 8 / G;
+    for (int h0 = 0; h0 < G; h0 += 8) {
+        const int h = G >= 8 ? h0 + warp : warp % G, grp = G >= 8 ? 0 : warp / G;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (h < G && grp < ng) {
+            const float m = head_m[h];
+            const float4 *op = reinterpret_cast<const float4 *>(opart + (slot0 * G + h) * kCacheD) + lane;
+#pragma unroll 8
+            for (int i = grp; i < np; i += ng) {
+                const float f = fast_exp2(__ldcg(ml + static_cast<size_t>(i) * G + h).x - m);
+                const float4 v = __ldcg(op + static_cast<size_t>(i) * G * (kCacheD / 4));
+                a.x = fmaf(f, v.x, a.x), a.y = fmaf(f, v.y, a.y), a.z = fmaf(f, v.z, a.z), a.w = fmaf(f, v.w, a.w);
+            }
+        }
+        if (ng > 1) {
+            part[warp][lane] = a;
+            __syncthreads();
+            if (grp == 0)
+                for (int i = 1; i < ng; ++i) {
+                    const float4 v = part[warp + i * G][lane];
+                    a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
+                }
+        }
+        if (h < G && grp == 0) {
+            const float inv = 1.f / head_l[h];
+            reinterpret_cast<uint2 *>(o + (static_cast<size_t>(bh) * G + h) * kCacheD)[lane] =
+                make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+        }
+    }
+    if (!weight_out) return;
+    const float *win = weight_in ? weight_in + static_cast<size_t>(bh) * nb : nullptr;
+    float *wout = weight_out + static_cast<size_t>(bh) * nb;
+    auto mass = [&](int slot, int slots) {  // attention weight of one attended block, over the group's heads
+        float w = 0.f;
+        const float2 *bl = block_ml + static_cast<size_t>(bh) * G * slots + slot;
+        for (int h = 0; h < G; ++h) {
+            const float2 a = __ldcg(bl + static_cast<size_t>(h) * slots);
+            w += a.y * fast_exp2(a.x - head_m[h]) / head_l[h];
+        }
+        return w;
+    };
+    if (k == 0) {
+        for (int j = tid; j < nb; j += 256) wout[j] = (win ? win[j] : 0.f) + (j < ns ? mass(j, nb) : 0.f);
+    } else {
+        for (int j = tid; j < nb; j += 256) wout[j] = win ? win[j] : 0.f;
+        __syncthreads();
+        for (int i = tid; i < ns; i += 256) {  // attended blocks are distinct
+            const int j = __ldcg(idx + static_cast<size_t>(bh) * k + i);
+            if (j >= 0 && j < nb) wout[j] += mass(i, k);
+        }
+    }
+}
+
+}  // namespace ssa

@@ -19,6 +19,9 @@
 #include "attn_bwd.cuh"
 #include "decode.cuh"
 #include "rope.cuh"
+#include "rope_axes.cuh"
+#include "cache8.cuh"
+#include "cache_decode.cuh"
 
 using namespace ssa;
 
@@ -77,6 +80,41 @@ ssa_status_t check_dims(const ssa_dims_t *dims, Shape &S, bool need_k) {
     return SSA_OK;
 }
 
+// Shapes of the 8-bit cache's calls: H query heads (any multiple of Hkv), T = capacity, k = 0 or blocks attended.
+ssa_status_t check_cache_dims(const ssa_dims_t *dims, Shape &S) {
+    if (!dims) return SSA_ERR_INVALID_ARG;
+    S.B = dims->B;
+    S.H = dims->H;
+    S.T = dims->T;
+    S.d = dims->d;
+    S.s = dims->s;
+    S.k = dims->k;
+    S.dtype = dims->dtype;
+    S.scale = dims->scale;
+    if (S.B < 1 || S.H < 1 || S.T < 1 || S.d < 1 || S.s < 1) return SSA_ERR_INVALID_ARG;
+    if (S.dtype != SSA_DT_BF16 && S.dtype != SSA_DT_FP32) return SSA_ERR_INVALID_ARG;
+    if (!(std::isfinite(S.scale) && S.scale > 0.f)) return SSA_ERR_INVALID_ARG;
+    S.Hk = dims->Hkv ? dims->Hkv : S.H;
+    if (S.Hk < 1 || S.H % S.Hk != 0) return SSA_ERR_INVALID_ARG;
+    if (S.dtype != SSA_DT_BF16 || S.d != kCacheD) return SSA_ERR_UNSUPPORTED;
+    if (S.s != 64 && S.s != 128) return SSA_ERR_UNSUPPORTED;
+    if (S.T % S.s != 0) return SSA_ERR_UNSUPPORTED;
+    S.nb = S.T / S.s;
+    if (S.k < 0 || S.k > S.nb) return SSA_ERR_INVALID_ARG;
+    if (S.nb > kTopMaxBlocks) return SSA_ERR_UNSUPPORTED;
+    S.G = S.H / S.Hk;
+    S.BH = static_cast<size_t>(S.B) * S.H;
+    S.BHk = static_cast<size_t>(S.B) * S.Hk;
+    S.krows = S.BHk * S.T;
+    if (S.krows > 0x7FFFFFFFull || S.BH > 0x7FFFFFFFull) return SSA_ERR_UNSUPPORTED;  // TMA row coordinates are int32
+    return SSA_OK;
+}
+
+// Query heads per key head padded to a kernel's, and the grid of cache_attend_kernel: the CTAs that its shared
+// memory lets reside at once.
+inline int cache_heads(int G) { return G <= 8 ? 8 : G <= 16 ? 16 : 32; }
+inline unsigned cache_grid(int G) { return kCacheSms * (G <= 8 ? 3u : 2u); }
+
 inline size_t align_up(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 // Layout of the inverse selection index (the `index` buffer of ssa_sparse_index, or
@@ -112,6 +150,24 @@ IndexWs carve_index(const Shape &S, const void *base) {
     p += align_up(S.krows * S.k * 4);
     W.order = reinterpret_cast<int32_t *>(p);
     return W;
+}
+
+// Layout of ssa_cache_decode's workspace.
+struct CacheWs {
+    size_t ml, blocks, bytes;  // byte offsets behind the partial outputs; size
+};
+CacheWs cache_ws(const Shape &S) {
+    CacheWs W;
+    const size_t slots = cache_partials(cache_grid(S.G), S.BHk) * S.G;
+    W.ml = align_up(slots * kCacheD * 4);
+    W.blocks = W.ml + align_up(slots * 8);
+    W.bytes = W.blocks + align_up(S.BH * (S.k > 0 ? S.k : S.nb) * 8);
+    return W;
+}
+
+size_t cache_ws_bytes(const Shape &S, int op) {
+    if (op == SSA_OP_CACHE_EVICT) return align_up(S.BHk * evict_list_ints(S.nb) * 4);
+    return S.G <= kCacheMaxGroup ? cache_ws(S).bytes : 0;
 }
 
 size_t ws_bytes_for(const Shape &S, int op) {
@@ -215,6 +271,36 @@ template <typename K>
 bool set_smem(K kernel, size_t bytes) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) ==
            cudaSuccess;
+}
+
+// Launch of a kernel that may start while the one before it on the stream still runs (it waits for that one
+// with grid_dependency_wait before it touches what that one writes or reads).
+template <typename... P, typename... A>
+bool launch_dependent(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st, A... args) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...) == cudaSuccess;
+}
+
+// e4m3 rows of 128 bytes, boxes of one block.
+bool make_tmap_codes(CUtensorMap *m, const void *base, size_t rows, int box_rows) {
+    EncodeTiledFn f = encode_fn();
+    if (!f) return false;
+    const cuuint64_t gdim[2] = {kCacheD, rows};
+    const cuuint64_t gstride[1] = {kCacheD};
+    const cuuint32_t box[2] = {kCacheD, static_cast<cuuint32_t>(box_rows)};
+    const cuuint32_t estride[2] = {1, 1};
+    return f(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), gdim, gstride, box, estride,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 unsigned grid_for(size_t n, unsigned per_block) {
@@ -384,6 +470,8 @@ extern "C" {
 
 size_t ssa_workspace_size(const ssa_dims_t *dims, int op) {
     Shape S;
+    if (op == SSA_OP_CACHE_DECODE || op == SSA_OP_CACHE_EVICT)
+        return check_cache_dims(dims, S) == SSA_OK ? cache_ws_bytes(S, op) : 0;
     const bool need_k = op == SSA_OP_SPARSE_FWD || op == SSA_OP_SPARSE_BWD;
     if (check_dims(dims, S, need_k) != SSA_OK) return 0;
     return ws_bytes_for(S, op);
@@ -753,6 +841,195 @@ ssa_status_t ssa_rope(const ssa_dims_t *dims, void *X, int heads, int pos0, floa
                                                          transpose ? 1 : 0);
     else
         rope_kernel<float><<<grid, 256, 0, st>>>((float *)X, heads, S.T, S.d, pos0, l2b, inv, transpose ? 1 : 0);
+    return launch_status();
+}
+
+ssa_status_t ssa_rope_axes(const ssa_dims_t *dims, const int32_t *pos, int axes, const int32_t *sections,
+                           unsigned flags, float base, float factor, const void *Q, const int64_t *q_strides, void *Qr,
+                           const int64_t *qr_strides, const void *K, const int64_t *k_strides, void *Kr,
+                           const int64_t *kr_strides, ssa_stream_t stream) {
+    if (!dims || !pos || !sections || (!Q && !K) || !Q != !Qr || !K != !Kr) return SSA_ERR_INVALID_ARG;
+    const int B = dims->B, T = dims->T, d = dims->d, H = dims->H, Hk = dims->Hkv ? dims->Hkv : dims->H;
+    if (B < 1 || T < 1 || d < 1 || H < 1 || Hk < 1 || axes < 1 || axes > kRopeMaxAxes) return SSA_ERR_INVALID_ARG;
+    if (dims->dtype != SSA_DT_BF16 && dims->dtype != SSA_DT_FP32) return SSA_ERR_INVALID_ARG;
+    if (flags & ~static_cast<unsigned>(SSA_ROPE_TRANSPOSE | SSA_ROPE_INTERLEAVED | SSA_ROPE_OWN_LADDER))
+        return SSA_ERR_INVALID_ARG;
+    if (!(base > 1.f) || !std::isfinite(base) || !(factor > 0.f) || !std::isfinite(factor)) return SSA_ERR_INVALID_ARG;
+    if (d != 64 && d != 128) return SSA_ERR_UNSUPPORTED;
+    const int half = d / 2;
+    int left[kRopeMaxAxes];
+    int64_t sum = 0;
+    for (int a = 0; a < axes; ++a) {
+        if (sections[a] < 1) return SSA_ERR_INVALID_ARG;
+        sum += sections[a];
+        left[a] = sections[a];
+    }
+    if (sum != half) return SSA_ERR_INVALID_ARG;
+    const int64_t BT = static_cast<int64_t>(B) * T;
+    if (BT > 0x7FFFFFFFll || H > 65536 || Hk > 65536) return SSA_ERR_UNSUPPORTED;
+    const int esz = dims->dtype == SSA_DT_BF16 ? 2 : 4;
+    // strides: rows of one tensor must not share elements when it is written; 16-byte accesses
+    auto tensor = [&](RopeAxesTensor &X, const void *in, const int64_t *is, void *out, const int64_t *os, int heads) {
+        X.in = in;
+        X.out = out;
+        X.heads = in ? heads : 0;
+        const int64_t contiguous[3] = {static_cast<int64_t>(heads) * T * d, static_cast<int64_t>(T) * d, d};
+        const int64_t extent[3] = {B, heads, T};
+        for (int i = 0; i < 3; ++i) {
+            X.is[i] = is ? is[i] : contiguous[i];
+            X.os[i] = os ? os[i] : contiguous[i];
+            if (extent[i] == 1) X.is[i] = X.os[i] = 0;
+        }
+        if (!in) return true;
+        for (int i = 0; i < 3; ++i) {
+            if (X.is[i] < 0 || X.is[i] * esz % 16 || X.os[i] * esz % 16) return false;
+            if (extent[i] > 1 && X.os[i] < d) return false;
+            if (in == out && X.is[i] != X.os[i]) return false;
+        }
+        return ((reinterpret_cast<uintptr_t>(in) | reinterpret_cast<uintptr_t>(out)) & 15u) == 0;
+    };
+    RopeAxesTensor XQ, XK;
+    if (!tensor(XQ, Q, q_strides, Qr, qr_strides, H) || !tensor(XK, K, k_strides, Kr, kr_strides, Hk))
+        return SSA_ERR_INVALID_ARG;
+    RopeAxesTable tab;
+    const double l2b = std::log2(static_cast<double>(base));
+    const double per = 1.0 / (6.283185307179586476925 * static_cast<double>(factor));
+    for (int i = 0, a = 0; i < half; ++i) {  // contiguous sections, or pairs dealt out in turn
+        while (left[a] == 0) a = (a + 1) % axes;
+        const int rank = sections[a] - left[a]--;
+        const double power = (flags & SSA_ROPE_OWN_LADDER) ? static_cast<double>(rank) / sections[a]
+                                                           : static_cast<double>(i) / half;
+        tab.axis[i] = static_cast<uint8_t>(a);
+        tab.turns[i] = std::exp2(-power * l2b) * per;
+        if (flags & SSA_ROPE_INTERLEAVED) a = (a + 1) % axes;
+    }
+    for (int i = half; i < 64; ++i) tab.axis[i] = 0, tab.turns[i] = 0.0;
+    // tokens per CTA: 16 where there are many (the angles are shared by the heads), down to one, so that two
+    // CTAs' worth per SM share the work; then the heads are split while SMs are still idle
+    const int heads = XQ.heads + XK.heads;
+    const int64_t want = (BT + 2 * kCacheSms - 1) / (2 * kCacheSms);
+    const int rows = static_cast<int>(want < 1 ? 1 : want > kRopeAxesRows ? kRopeAxesRows : want);
+    const int64_t ctas = (BT + rows - 1) / rows;
+    int slices = static_cast<int>(2 * kCacheSms / ctas);
+    slices = slices < 1 ? 1 : slices > (heads + 7) / 8 ? (heads + 7) / 8 : slices;
+    const int per_slice = (heads + slices - 1) / slices;
+    const dim3 grid(static_cast<unsigned>(ctas), (heads + per_slice - 1) / per_slice);
+    const float sign = (flags & SSA_ROPE_TRANSPOSE) ? -1.f : 1.f;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (dims->dtype == SSA_DT_BF16)
+        rope_axes_kernel<__nv_bfloat16><<<grid, kRopeAxesThreads, 0, st>>>(tab, pos, BT, T, half, rows, per_slice, sign, XQ,
+                                                                           XK);
+    else
+        rope_axes_kernel<float><<<grid, kRopeAxesThreads, 0, st>>>(tab, pos, BT, T, half, rows, per_slice, sign, XQ, XK);
+    return launch_status();
+}
+
+ssa_status_t ssa_cache_append(const ssa_dims_t *dims, int n, const int32_t *cache_len, const int32_t *n_new,
+                              const void *K, const int64_t *k_strides, const void *V, const int64_t *v_strides,
+                              void *K8, float *Kscale, void *V8, float *Vscale, float *Kbar, ssa_stream_t stream) {
+    Shape S;
+    const ssa_status_t e = check_cache_dims(dims, S);
+    if (e != SSA_OK) return e;
+    if (!cache_len || !K || !V || !K8 || !Kscale || !V8 || !Vscale || n < 1 || n > S.T) return SSA_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(K) | reinterpret_cast<uintptr_t>(V) | reinterpret_cast<uintptr_t>(K8) |
+         reinterpret_cast<uintptr_t>(V8)) & 15u)
+        return SSA_ERR_INVALID_ARG;
+    CacheRows X[2];
+    for (int i = 0; i < 2; ++i) {
+        const int64_t *st = i ? v_strides : k_strides;
+        X[i].p = static_cast<const __nv_bfloat16 *>(i ? V : K);
+        const int64_t contiguous[3] = {static_cast<int64_t>(S.Hk) * n * S.d, static_cast<int64_t>(n) * S.d, S.d};
+        const int64_t extent[3] = {S.B, S.Hk, n};
+        for (int a = 0; a < 3; ++a) {
+            X[i].st[a] = extent[a] == 1 ? 0 : st ? st[a] : contiguous[a];
+            if (X[i].st[a] < 0 || X[i].st[a] % 8) return SSA_ERR_INVALID_ARG;  // 16-byte reads
+        }
+    }
+    int blocks = (n + S.s - 2) / S.s + 1;
+    if (blocks > S.nb) blocks = S.nb;
+    const dim3 grid(static_cast<unsigned>(S.BHk), blocks, 2);
+    auto kernel = S.s == 128 ? cache_append_kernel<128> : cache_append_kernel<64>;
+    kernel<<<grid, 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+        cache_len, n_new, n, X[0], X[1], static_cast<uint8_t *>(K8), Kscale, static_cast<uint8_t *>(V8), Vscale, Kbar,
+        S.Hk, S.T);
+    return launch_status();
+}
+
+ssa_status_t ssa_cache_decode(const ssa_dims_t *dims, const int32_t *cache_len, const void *q, const void *K8,
+                              const float *Kscale, const void *V8, const float *Vscale, const float *Kbar, int32_t *idx,
+                              void *o, float *lse, const float *weight_in, float *weight_out, void *ws, size_t ws_bytes,
+                              ssa_stream_t stream) {
+    Shape S;
+    const ssa_status_t e = check_cache_dims(dims, S);
+    if (e != SSA_OK) return e;
+    if (!cache_len || !q || !K8 || !Kscale || !V8 || !Vscale || !o || !lse) return SSA_ERR_INVALID_ARG;
+    if ((S.k > 0 && !idx) || (S.k > 1 && !Kbar) || (weight_in && !weight_out)) return SSA_ERR_INVALID_ARG;
+    if (S.G > kCacheMaxGroup) return SSA_ERR_UNSUPPORTED;
+    if ((reinterpret_cast<uintptr_t>(K8) | reinterpret_cast<uintptr_t>(V8) | reinterpret_cast<uintptr_t>(q) |
+         reinterpret_cast<uintptr_t>(o) | reinterpret_cast<uintptr_t>(Kbar)) & 15u)
+        return SSA_ERR_INVALID_ARG;
+    const CacheWs W = cache_ws(S);
+    if (!ws || ws_bytes < W.bytes || (reinterpret_cast<uintptr_t>(ws) & 15u)) return SSA_ERR_WORKSPACE;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    float *opart = static_cast<float *>(ws);
+    float2 *ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(ws) + W.ml);
+    float2 *block_ml = weight_out ? reinterpret_cast<float2 *>(static_cast<uint8_t *>(ws) + W.blocks) : nullptr;
+    const unsigned bhk = static_cast<unsigned>(S.BHk);
+    const __nv_bfloat16 *qb = static_cast<const __nv_bfloat16 *>(q);
+    CUtensorMap tmK, tmV;
+    if (!make_tmap_codes(&tmK, K8, S.krows, S.s) || !make_tmap_codes(&tmV, V8, S.krows, S.s)) return SSA_ERR_CUDA;
+    if (S.k > 0)
+        cache_select_kernel<<<bhk, kTopThreads, static_cast<size_t>(S.nb) * 4, st>>>(cache_len, qb, Kbar, idx, S.Hk, S.G,
+                                                                                    S.T, S.s, S.k, S.nb);
+    auto attend = [&](auto kernel, size_t smem) {
+        if (!set_smem(kernel, smem)) return false;
+        const dim3 grid(cache_grid(S.G));
+        const float scale_log2 = static_cast<float>(S.scale * 1.4426950408889634);
+        if (S.k > 0)
+            return launch_dependent(kernel, grid, 128, smem, st, tmK, tmV, cache_len, qb, Kscale, Vscale, idx, opart, ml,
+                                    block_ml, S.B, S.Hk, S.G, S.T, S.s, S.k, S.nb, scale_log2);
+        kernel<<<grid, 128, smem, st>>>(tmK, tmV, cache_len, qb, Kscale, Vscale, idx, opart, ml, block_ml, S.B, S.Hk, S.G,
+                                        S.T, S.s, S.k, S.nb, scale_log2);
+        return true;
+    };
+    const int NH = cache_heads(S.G);
+    const bool ok = NH == 8    ? attend(cache_attend_kernel<8>, CacheAttendSmem<8>::kTotal)
+                    : NH == 16 ? attend(cache_attend_kernel<16>, CacheAttendSmem<16>::kTotal)
+                               : attend(cache_attend_kernel<32>, CacheAttendSmem<32>::kTotal);
+    if (!ok) return SSA_ERR_CUDA;
+    if (!launch_dependent(cache_combine_kernel, dim3(bhk), 256, 0, st, cache_len, opart, ml, block_ml, idx,
+                          static_cast<__nv_bfloat16 *>(o), lse, weight_in, weight_out, S.B, S.Hk, S.G, S.T, S.s, S.k, S.nb,
+                          static_cast<int>(cache_grid(S.G))))
+        return SSA_ERR_CUDA;
+    return launch_status();
+}
+
+ssa_status_t ssa_cache_evict(const ssa_dims_t *dims, int keep, int sink, int recent, const int32_t *cache_len,
+                             int32_t *new_len, const float *weight_in, float *weight_out, void *K8, float *Kscale,
+                             void *V8, float *Vscale, float *Kbar, int32_t *kept, void *ws, size_t ws_bytes,
+                             ssa_stream_t stream) {
+    Shape S;
+    const ssa_status_t e = check_cache_dims(dims, S);
+    if (e != SSA_OK) return e;
+    if (!cache_len || !weight_in || !K8 || !Kscale || !V8 || !Vscale || !kept) return SSA_ERR_INVALID_ARG;
+    if (keep < 1 || keep > S.nb || sink < 0 || recent < 0 || sink > keep || recent > keep - sink)
+        return SSA_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(K8) | reinterpret_cast<uintptr_t>(V8) | reinterpret_cast<uintptr_t>(Kbar)) & 15u)
+        return SSA_ERR_INVALID_ARG;
+    if (!ws || ws_bytes < cache_ws_bytes(S, SSA_OP_CACHE_EVICT) || (reinterpret_cast<uintptr_t>(ws) & 15u))
+        return SSA_ERR_WORKSPACE;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    int32_t *lists = static_cast<int32_t *>(ws);
+    const unsigned bhk = static_cast<unsigned>(S.BHk);
+    const size_t sm = (2 * static_cast<size_t>(S.nb) + keep + 1) * 4, sm_move = static_cast<size_t>(S.nb) * 4;
+    if (!set_smem(cache_evict_select_kernel, sm)) return SSA_ERR_CUDA;
+    cache_evict_select_kernel<<<bhk, kTopThreads, sm, st>>>(cache_len, weight_in, weight_out, Kscale, Vscale, kept, lists,
+                                                            S.Hk, S.T, S.s, S.nb, keep, sink, recent);
+    const int columns = 2 * S.s * (kCacheD / 16) + (Kbar ? kCacheD * 4 / 16 : 0);
+    if (!launch_dependent(cache_evict_move_kernel, dim3(bhk, (columns + kMoveThreads - 1) / kMoveThreads), kMoveThreads,
+                          sm_move, st, static_cast<uint8_t *>(K8), static_cast<uint8_t *>(V8), Kbar, new_len, lists, S.Hk,
+                          S.s, S.nb))
+        return SSA_ERR_CUDA;
     return launch_status();
 }
 

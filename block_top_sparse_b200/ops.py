@@ -14,7 +14,7 @@ the other stream only receives the alignment gradient.
 """
 from __future__ import annotations
 
-from typing import Dict, Optional
+from typing import Dict, NamedTuple, Optional
 
 import torch
 
@@ -101,6 +101,146 @@ def rope(dims: L.Dims, X: torch.Tensor, pos0: int = 0, base: float = 10000.0, fa
                L.SSA_DT_FP32 if X.dtype == torch.float32 else L.SSA_DT_BF16, dims.scale, dims.Hkv)
     L.ssa_rope(d, X, X.shape[1], pos0, base, factor, int(transpose))
     return X
+
+
+def _is(t: torch.Tensor, name: str, shape, dtype, device, strided: bool = False) -> None:
+    """ValueError unless t is what the call reads: the library sees its address only."""
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device:
+        raise ValueError("%s must be %s %s on %s, got %s %s on %s" % (name, list(shape), dtype, device, list(t.shape),
+                                                                      t.dtype, t.device))
+    if not strided and not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+
+
+def _device_of(t: torch.Tensor) -> torch.device:
+    """The device that a call runs on: its tensors' device, which must be the current one."""
+    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+        raise ValueError("tensors must be on the current CUDA device, got %s" % t.device)
+    return t.device
+
+
+def rope_axes(dims: L.Dims, pos: torch.Tensor, sections, Q: torch.Tensor, K: Optional[torch.Tensor] = None,
+              base: float = 10000.0, factor: float = 1.0, interleaved: bool = False, own_ladder: bool = False,
+              transpose: bool = False, out=None):
+    """Rotary positions with several axes on Q [B, H, T, d] and K [B, Hkv, T, d] (bf16 or fp32, also strided views
+    such as a transposed projection); pos [axes, B, T] int32, sections = pairs of every axis (ssa_rope_axes).
+    out: the pair of tensors to write, (Q, K) for in place; default: new contiguous ones.  Returns (Qr, Kr)."""
+    dev = _device_of(Q)
+    dtype = Q.dtype
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("Q must be bf16 or fp32, got %s" % dtype)
+    shape = (dims.B, dims.H, dims.T, dims.d)
+    kshape = (dims.B, dims.kv_heads, dims.T, dims.d)
+    _is(Q, "Q", shape, dtype, dev, True)
+    _is(pos, "pos", (len(sections), dims.B, dims.T), torch.int32, dev)
+    if K is not None:
+        _is(K, "K", kshape, dtype, dev, True)
+    if out is None:
+        Qr = torch.empty(shape, dtype=dtype, device=dev)
+        Kr = None if K is None else torch.empty(kshape, dtype=dtype, device=dev)
+    else:
+        Qr, Kr = out
+        _is(Qr, "out[0]", shape, dtype, dev, True)
+        if (K is None) != (Kr is None):
+            raise ValueError("out must hold a tensor for K exactly when K is given")
+        if Kr is not None:
+            _is(Kr, "out[1]", kshape, dtype, dev, True)
+    d = L.Dims(dims.B, dims.H, dims.T, dims.d, dims.s, dims.k,
+               L.SSA_DT_FP32 if dtype == torch.float32 else L.SSA_DT_BF16, dims.scale, dims.Hkv)
+    flags = ((L.SSA_ROPE_TRANSPOSE if transpose else 0) | (L.SSA_ROPE_INTERLEAVED if interleaved else 0)
+             | (L.SSA_ROPE_OWN_LADDER if own_ladder else 0))
+    L.ssa_rope_axes(d, pos, sections, Q, Qr, K, Kr, flags, base, factor)
+    return Qr, Kr
+
+
+class Cache8(NamedTuple):
+    """An 8-bit key/value cache: codes [B, Hkv, T, d] (float8_e4m3fn), scales [B, Hkv, T/s] fp32 and, for sparse
+    decoding, the pooled keys [B, Hkv, T/s, d] fp32 (None: not kept)."""
+    K8: torch.Tensor
+    Kscale: torch.Tensor
+    V8: torch.Tensor
+    Vscale: torch.Tensor
+    Kbar: Optional[torch.Tensor] = None
+
+    @staticmethod
+    def empty(dims: L.Dims, device="cuda", pooled: bool = True) -> "Cache8":
+        """Buffers for dims.B sequences of up to dims.T tokens (contents undefined, as no token is held yet)."""
+        B, Hk, nb = dims.B, dims.kv_heads, dims.T // dims.s
+        codes = lambda: torch.empty((B, Hk, dims.T, dims.d), dtype=torch.float8_e4m3fn, device=device)  # noqa: E731
+        scale = lambda: torch.empty((B, Hk, nb), dtype=torch.float32, device=device)  # noqa: E731
+        return Cache8(codes(), scale(), codes(), scale(),
+                      torch.empty((B, Hk, nb, dims.d), dtype=torch.float32, device=device) if pooled else None)
+
+    def check(self, dims: L.Dims, device) -> None:
+        B, Hk, nb = dims.B, dims.kv_heads, dims.T // dims.s
+        for name, codes, scale in (("K", self.K8, self.Kscale), ("V", self.V8, self.Vscale)):
+            _is(codes, name + "8", (B, Hk, dims.T, dims.d), torch.float8_e4m3fn, device)
+            _is(scale, name + "scale", (B, Hk, nb), torch.float32, device)
+        if self.Kbar is not None:
+            _is(self.Kbar, "Kbar", (B, Hk, nb, dims.d), torch.float32, device)
+
+
+def cache_append(dims: L.Dims, cache: Cache8, cache_len: torch.Tensor, K: torch.Tensor, V: torch.Tensor,
+                 n_new: Optional[torch.Tensor] = None) -> None:
+    """Writes the tokens K, V [B, Hkv, n, d] (bf16, also strided views) at cache_len [B] (int32) of every sequence,
+    n_new[b] of them (default: n).  The caller advances cache_len, once for all layers."""
+    dev = _device_of(K)
+    shape = (dims.B, dims.kv_heads, K.shape[2], dims.d)
+    _is(K, "K", shape, torch.bfloat16, dev, True)
+    _is(V, "V", shape, torch.bfloat16, dev, True)
+    _is(cache_len, "cache_len", (dims.B,), torch.int32, dev)
+    if n_new is not None:
+        _is(n_new, "n_new", (dims.B,), torch.int32, dev)
+    cache.check(dims, dev)
+    L.ssa_cache_append(dims, cache_len, K, V, cache.K8, cache.Kscale, cache.V8, cache.Vscale, cache.Kbar, n_new)
+
+
+def cache_decode(dims: L.Dims, cache: Cache8, cache_len: torch.Tensor, q: torch.Tensor,
+                 weight_in: Optional[torch.Tensor] = None, weight_out: Optional[torch.Tensor] = None,
+                 ws: Optional[torch.Tensor] = None):
+    """Attention of q [B, H, d] (bf16), the token at position cache_len[b] of every sequence, over the 8-bit cache:
+    all tokens (dims.k == 0) or dims.k selected blocks.  weight_out [B, Hkv, T/s] receives weight_in (or 0) plus
+    every block's attention weight; the same tensor for both adds in place.  Returns (o, lse, idx); idx is None for
+    dims.k == 0."""
+    dev = _device_of(q)
+    _is(q, "q", (dims.B, dims.H, dims.d), torch.bfloat16, dev)
+    _is(cache_len, "cache_len", (dims.B,), torch.int32, dev)
+    cache.check(dims, dev)
+    for name, w in (("weight_in", weight_in), ("weight_out", weight_out)):
+        if w is not None:
+            _is(w, name, (dims.B, dims.kv_heads, dims.T // dims.s), torch.float32, dev)
+    o = torch.empty_like(q)
+    lse = torch.empty((dims.B, dims.H), dtype=torch.float32, device=dev)
+    idx = torch.empty((dims.B, dims.kv_heads, dims.k), dtype=torch.int32, device=dev) if dims.k > 0 else None
+    if ws is None:
+        ws = _ws(dims, L.SSA_OP_CACHE_DECODE, dev)
+    L.ssa_cache_decode(dims, cache_len, q, cache.K8, cache.Kscale, cache.V8, cache.Vscale, cache.Kbar, idx, o, lse,
+                       weight_in, weight_out, ws)
+    return o, lse, idx
+
+
+def cache_evict(dims: L.Dims, cache: Cache8, cache_len: torch.Tensor, keep: int, weight: torch.Tensor, sink: int = 0,
+                recent: int = 0, weight_out: Optional[torch.Tensor] = None, new_len: Optional[torch.Tensor] = None,
+                ws: Optional[torch.Tensor] = None):
+    """Keeps `keep` complete blocks of every sequence and key/value head: the first `sink`, the last `recent` and the
+    ones of greatest weight [B, Hkv, T/s]; the cache is compacted in place.  weight_out (may be weight) receives the
+    weights in the new order, new_len (default: a new tensor; may be cache_len) the lengths.  Returns (kept, new_len)."""
+    dev = _device_of(weight)
+    _is(weight, "weight", (dims.B, dims.kv_heads, dims.T // dims.s), torch.float32, dev)
+    _is(cache_len, "cache_len", (dims.B,), torch.int32, dev)
+    cache.check(dims, dev)
+    if weight_out is not None:
+        _is(weight_out, "weight_out", weight.shape, torch.float32, dev)
+    if new_len is None:
+        new_len = torch.empty_like(cache_len)
+    else:
+        _is(new_len, "new_len", (dims.B,), torch.int32, dev)
+    kept = torch.empty((dims.B, dims.kv_heads, max(int(keep), 0)), dtype=torch.int32, device=dev)
+    if ws is None:
+        ws = _ws(dims, L.SSA_OP_CACHE_EVICT, dev)
+    L.ssa_cache_evict(dims, keep, cache_len, weight, cache.K8, cache.Kscale, cache.V8, cache.Vscale, kept, cache.Kbar,
+                      weight_out, new_len, sink, recent, ws)
+    return kept, new_len
 
 
 def dropped_mass(dims: L.Dims, lse_sparse, lse_full) -> torch.Tensor:

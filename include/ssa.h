@@ -86,7 +86,16 @@ enum {
     SSA_OP_FULL_BWD = 3,
     SSA_OP_ALIGN_FWD = 4,
     SSA_OP_SPARSE_INDEX = 5, /* bytes of the `index` buffer of ssa_sparse_index */
-    SSA_OP_DECODE = 6        /* workspace of ssa_sparse_decode */
+    SSA_OP_DECODE = 6,       /* workspace of ssa_sparse_decode */
+    SSA_OP_CACHE_DECODE = 7, /* workspace of ssa_cache_decode */
+    SSA_OP_CACHE_EVICT = 8   /* workspace of ssa_cache_evict */
+};
+
+/* ssa_rope_axes flags. */
+enum {
+    SSA_ROPE_TRANSPOSE = 1u,   /* turn back: maps gradients of the rotated tensors to those of their inputs */
+    SSA_ROPE_INTERLEAVED = 2u, /* pairs dealt out to the axes in turn instead of section by section */
+    SSA_ROPE_OWN_LADDER = 4u   /* every axis runs through all frequencies instead of sharing one ladder */
 };
 
 /* ssa_block_select flags. */
@@ -335,6 +344,122 @@ ssa_status_t ssa_sparse_decode(const ssa_dims_t *dims, const int32_t *cache_len,
  */
 ssa_status_t ssa_rope(const ssa_dims_t *dims, void *X, int heads, int pos0, float base, float factor, int transpose,
                       ssa_stream_t stream);
+
+/*
+ * Rotary positions with several axes (time, height and width of images and
+ * video; no counterpart in the paper), on the queries and keys of a layer in
+ * one call.  Token t of sequence b has the position pos[a][b][t] on axis a.  The
+ * d/2 pairs (x_i, x_{i+d/2}) of a row belong to one axis each: sections[a] of
+ * them to axis a, sum of sections = d/2, either section by section (pairs
+ * 0 .. sections[0]-1 to axis 0, and so on) or, with SSA_ROPE_INTERLEAVED, dealt
+ * out in turn (0, 1, 2, 0, 1, 2, ..), an axis being passed over once its section
+ * is full.  Pair i turns by pos * base^(-i/(d/2)) / factor, or with
+ * SSA_ROPE_OWN_LADDER by pos * base^(-r/sections[a]) / factor, r = how many of
+ * the axis's pairs come before it.  One axis with positions pos0 + t is ssa_rope.
+ *   dims       B, H, Hkv, T >= 1 (any length, one token per sequence too), d = 64
+ *              or 128, dtype; s, k and scale are not read
+ *   pos        in  [axes, B, T] int32, device; any values
+ *   axes       1 .. 4;  sections: host array of `axes` entries >= 1
+ *   Q, K       in  [B, H, T, d], [B, Hkv, T, d]; Qr, Kr out, the same shapes, or
+ *              the inputs themselves (then with their strides); otherwise they
+ *              must not overlap the inputs.  Either tensor may be NULL with its output.
+ *   *_strides  host arrays of 3: elements from one sequence, head, token to the
+ *              next (a row's d elements are adjacent); NULL: contiguous.  Rows
+ *              of a projection ([B, T, heads, d]) need no copy.  Strides are
+ *              multiples of 16 bytes and >= 0, those of outputs >= d and such
+ *              that no two rows overlap; base addresses are 16-byte aligned.
+ */
+ssa_status_t ssa_rope_axes(const ssa_dims_t *dims, const int32_t *pos, int axes, const int32_t *sections,
+                           unsigned flags, float base, float factor, const void *Q, const int64_t *q_strides, void *Qr,
+                           const int64_t *qr_strides, const void *K, const int64_t *k_strides, void *Kr,
+                           const int64_t *kr_strides, ssa_stream_t stream);
+
+/*
+ * The 8-bit key/value cache (no counterpart in the paper): e4m3 codes
+ * K8, V8 [B, Hkv, T, d] and one fp32 scale per block of s tokens and key/value
+ * head, Kscale, Vscale [B, Hkv, T/s]; an element is code * scale.  Half the
+ * bytes of a bf16 cache, and so half the time of reading it.  The scale of a
+ * block is a power of two, so that an element carries one rounding to e4m3 (at
+ * most 2^-4 of its value; multiples of 2^-9 scale below 2^-6 scale).  Kbar
+ * [B, Hkv, T/s, d] fp32 holds the mean keys of the complete blocks, as for
+ * ssa_sparse_decode.
+ *
+ * Shapes of the three calls below: dtype bf16, d = 128, s in {64, 128}, T =
+ * capacity in tokens, T % s == 0, T/s <= 8192, B*Hkv*T < 2^31; H any multiple of
+ * Hkv.  cache_len [B] int32 (device) counts the tokens that come before those of
+ * the call, as for ssa_sparse_decode: append at cache_len, decode at cache_len,
+ * then the caller adds the new tokens, once for all layers.  Codes (and q, o,
+ * Kbar) need 16-byte aligned base addresses.  Rows behind the last token may hold
+ * anything; no call writes them.
+ *
+ * ssa_cache_append writes n_new[b] tokens of sequence b (NULL: n for all; 0
+ * allowed) at positions cache_len[b] ..
+ *   K, V       in  [B, Hkv, n, d] bf16, n >= 1; strides as for ssa_rope_axes
+ *              (NULL: contiguous); rows from n_new[b] on are not read
+ *   n_new      in  [B] int32 or NULL
+ *   K8, Kscale, V8, Vscale  in/out.  The scale of a touched block is the smallest
+ *              2^p >= 2^-126 with max |x| / 2^p <= 448 over the call's finite
+ *              elements in it, or the block's present one if that is larger and
+ *              the block holds older tokens; if it grows, the older codes are
+ *              rounded again at the new scale.  Infinities and NaN are stored as NaN.
+ *   Kbar       in/out, or NULL: row j is written when the call completes block j,
+ *              with the mean of the keys as the cache holds them
+ * A sequence with cache_len < 0, n_new outside [0, n] or more than T tokens in
+ * all records SSA_ERR_BAD_INPUT and keeps its cache as it was.
+ */
+ssa_status_t ssa_cache_append(const ssa_dims_t *dims, int n, const int32_t *cache_len, const int32_t *n_new,
+                              const void *K, const int64_t *k_strides, const void *V, const int64_t *v_strides,
+                              void *K8, float *Kscale, void *V8, float *Vscale, float *Kbar, ssa_stream_t stream);
+
+/*
+ * Attention of one new token per sequence over the 8-bit cache; its key and value
+ * sit at position L = cache_len[b] already.  -1 <= L < T; L = -1 is an idle
+ * row of the batch: o = 0, lse = -inf, idx = -1, weight unchanged.
+ *   dims       H/Hkv <= 32 query heads per key/value head; scale;
+ *              k = 0: attend every token up to L;
+ *              k >= 1 (<= T/s): the block of L and the k-1 blocks before it with the
+ *              highest scores (sum of the group's queries) . Kbar_j, summed in 64
+ *              bits and rounded to fp32; ties to the lower index
+ *   q          in  [B, H, d] bf16
+ *   Kbar       in  for k >= 2 (else may be NULL): rows before the block of L are read
+ *   idx        out [B, Hkv, k] int32, ascending, -1 behind; NULL allowed for k = 0
+ *   o          out [B, H, d] bf16;  lse out [B, H] fp32
+ *   weight_in, weight_out  [B, Hkv, T/s] fp32: weight_out[j] = weight_in[j] + the
+ *              attention weight of block j's tokens, summed over the group's heads
+ *              (weight_in NULL: 0; the same buffer: added in place); both NULL: none
+ *   ws         >= ssa_workspace_size(dims, SSA_OP_CACHE_DECODE) bytes
+ * A cache length outside [-1, T) records SSA_ERR_BAD_INPUT; its row counts as idle.
+ */
+ssa_status_t ssa_cache_decode(const ssa_dims_t *dims, const int32_t *cache_len, const void *q, const void *K8,
+                              const float *Kscale, const void *V8, const float *Vscale, const float *Kbar, int32_t *idx,
+                              void *o, float *lse, const float *weight_in, float *weight_out, void *ws, size_t ws_bytes,
+                              ssa_stream_t stream);
+
+/*
+ * Eviction by accumulated attention weight, whole blocks at a time, in place.  A
+ * head of a sequence with more than `keep` complete blocks keeps the first `sink`
+ * and the last `recent` of them and those of greatest weight among the others,
+ * `keep` in all (equal weights: the lower index stays; NaN counts least).  The kept
+ * blocks move down in order, with their codes, scales, pooled keys and weights, and
+ * the block begun behind them follows.  Tokens keep the rotary positions that their
+ * keys were written with; the sequence's new length counts cache rows only.
+ *   keep       1 .. T/s;  sink, recent >= 0, sink + recent <= keep
+ *   cache_len  in  [B] int32, tokens that the cache holds, 0 .. T
+ *   new_len    out [B] int32 or NULL: keep * s + cache_len % s, or cache_len where
+ *              nothing left; may be cache_len itself
+ *   weight_in  in  [B, Hkv, T/s] fp32;  weight_out out or NULL: the weights in the
+ *              blocks' new order, 0 behind them; may be weight_in itself
+ *   K8, Kscale, V8, Vscale, Kbar (or NULL)  in/out
+ *   kept       out [B, Hkv, keep] int32: former indices of the complete blocks,
+ *              ascending, -1 behind
+ *   ws         >= ssa_workspace_size(dims, SSA_OP_CACHE_EVICT) bytes
+ * A cache length outside [0, T] records SSA_ERR_BAD_INPUT; that sequence stays as it
+ * was (kept = -1).
+ */
+ssa_status_t ssa_cache_evict(const ssa_dims_t *dims, int keep, int sink, int recent, const int32_t *cache_len,
+                             int32_t *new_len, const float *weight_in, float *weight_out, void *K8, float *Kscale,
+                             void *V8, float *Vscale, float *Kbar, int32_t *kept, void *ws, size_t ws_bytes,
+                             ssa_stream_t stream);
 
 /*
  * Self-test of the hang guard (no counterpart in the paper).  Every wait of the
