@@ -135,19 +135,16 @@ __host__ __device__ __forceinline__ size_t cache_partials(size_t ctas, size_t pa
 // Position in the sequence of tiles: pair (b, hk), tile t of its nt.
 struct TilePos {
     int b, hk, t, nt, L;
-    __device__ __forceinline__ void enter(int b_, const int32_t *cache_len, int B, int T, int s, int k) {
-        for (b = b_; b < B; ++b) {
-            L = __ldg(cache_len + b);
-            nt = cache_tiles(L, T, s, k);
-            if (nt > 0) break;
-        }
-        hk = t = 0;
-    }
     __device__ __forceinline__ void next(const int32_t *cache_len, int B, int Hk, int T, int s, int k) {
         if (++t < nt) return;
         t = 0;
         if (++hk < Hk) return;
-        enter(b + 1, cache_len, B, T, s, k);
+        hk = 0;
+        for (++b; b < B; ++b) {
+            L = __ldg(cache_len + b);
+            nt = cache_tiles(L, T, s, k);
+            if (nt > 0) return;
+        }
     }
 };
 
@@ -204,48 +201,59 @@ __device__ __forceinline__ TilePos cache_locate(const int32_t *cache_len, int64_
     return p;
 }
 
+// Query heads per key head are padded to NH = 4, 8, 16 or 32.
 template <int NH>
-struct CacheAttendSmem {
-    static constexpr int kStages = 2;
+struct CacheAttend {
     static constexpr int kTile = 128 * kCacheD;                      // 16 KB: keys or values of one tile
-    static constexpr int kNS = 2 * NH;                               // columns of the logits' product
+    static constexpr int kNS = NH < 8 ? 16 : 2 * NH;                 // columns of the logits' product (term * NH + head)
     static constexpr int kNP = (3 * NH + 15) / 16 * 16;              // columns of the output's product
-    static constexpr int kQ = kStages * 2 * kTile;                   // [kNS][128 B]
+    static constexpr int kQ = 2 * kTile;                             // [kNS][128 B]
     static constexpr int kP = kQ + kNS * 128;                        // [kNP][128 B]
-    static constexpr int kMax = kP + kNP * 128;                      // [NH][4 warps] fp32
-    static constexpr int kSum = kMax + NH * 16;                      // [NH][4 warps] fp32
-    static constexpr int kHead = kSum + NH * 16;                     // [NH] logit factor, [NH] max, [NH] sum
+    static constexpr int kRed = kP + kNP * 128;                      // two of: [NH][4 warps] maxima, [NH][4 warps] sums
+    static constexpr int kHead = kRed + 2 * 2 * NH * 16;             // [NH] logit factor, [NH] maximum, [NH] sum
     static constexpr int kBar = kHead + 3 * NH * 4;
-    static constexpr int kTotal = kBar + 128 + 1024;                 // + alignment of the dynamic base to 1024 B
-    static constexpr int kTmemO = kNS;                               // first column of the output's product
-    static constexpr int kTmemCols = kNS + kNP <= 64 ? 64 : kNS + kNP <= 128 ? 128 : 256;
+    static constexpr int kBytes = kBar + 64 + 1024;                  // + alignment of the dynamic base to 1024 B
+    // the logits' columns may be written again while the outputs are read, except at NH = 32, where both
+    // products would take 256 columns a CTA and the outputs take the logits' place
+    static constexpr bool kApart = NH < 32;
+    static constexpr int kTmemO = kApart ? kNS : 0;                  // first column of the output's product
+    static constexpr int kCols = kTmemO + kNP;
+    static constexpr int kTmemCols = kCols <= 32 ? 32 : kCols <= 64 ? 64 : 128;
+    // CTAs per SM: shared memory (33 KB of keys and values and 4 to 20 KB of operands each) and, from NH = 16
+    // on, registers and tensor memory
+    static constexpr int kPerSm = NH <= 8 ? 5 : NH == 16 ? 4 : 3;
 };
 
 // Tile of 128 keys (one block of 128 or two of 64):
 //   S^T [128 keys x 2 NH] = K8 . (q terms)^T      A: keys as loaded (K-major), thread = key
 //   weights of the thread's key against the running maxima, split into three terms
 //   O^T [128 dims x 3 NH] = V8^T . (p terms)^T    A: values as loaded (M-major), thread = dim
-// The running maxima and the outputs stay in registers; only O^T of one tile is in tensor memory.
-template <int NH>
-__global__ void __launch_bounds__(128) cache_attend_kernel(
+// The outputs stay in registers, brought to the new maximum tile by tile; only O^T of one tile is in tensor
+// memory.  A tile is a chain of dependent steps (product, maximum, weights, product, output), so the CTA is
+// kept small -- one tile of keys and one of values, each loaded again as soon as its product has read it --
+// and up to five CTAs per SM run their chains beside one another's loads: 160 KB in flight or in use per SM.
+// (Two tiles of each and three CTAs per SM: 786 us instead of 498 us for 64 caches of 16K to 32K tokens, 8 key
+// heads, G = 4.)
+template <int NH, int S>
+__global__ void __launch_bounds__(128, CacheAttend<NH>::kPerSm) cache_attend_kernel(
     const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
     const int32_t *__restrict__ cache_len, const __nv_bfloat16 *__restrict__ q, const float *__restrict__ Kscale,
     const float *__restrict__ Vscale, const int32_t *idx, float *__restrict__ opart, float2 *__restrict__ mlpart,
-    float2 *__restrict__ block_ml, int B, int Hk, int G, int T, int s, int k, int nb, float scale_log2) {
-    using SM = CacheAttendSmem<NH>;
+    float2 *__restrict__ block_ml, int B, int Hk, int G, int T, int k, int nb, float scale_log2) {
+    using SM = CacheAttend<NH>;
+    constexpr int kPer = 128 / S;  // blocks of a tile
     extern __shared__ __align__(1024) uint8_t cad_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(cad_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const uint32_t sQ = smem_u32(smem + SM::kQ), sP = smem_u32(smem + SM::kP);
-    float *red_m = reinterpret_cast<float *>(smem + SM::kMax), *red_l = reinterpret_cast<float *>(smem + SM::kSum);
+    const uint32_t sK = smem_u32(smem), sV = sK + SM::kTile, sQ = sK + SM::kQ, sP = sK + SM::kP;
     float *head_f = reinterpret_cast<float *>(smem + SM::kHead), *head_m = head_f + NH, *head_l = head_m + NH;
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + SM::kBar);
-    uint64_t *bar_k = bars, *bar_v = bars + 2, *bar_s = bars + 4, *bar_o = bars + 5;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 6);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + 7);
+    uint64_t *bar_k = bars, *bar_v = bars + 1, *bar_s = bars + 2, *bar_o = bars + 3;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 4);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + 5);
 
     // this CTA's share of the tiles
-    const int64_t total = cache_total_tiles(cache_len, B, Hk, T, s, k, lane);
+    const int64_t total = cache_total_tiles(cache_len, B, Hk, T, S, k, lane);
     if (blockIdx.x == 0)
         for (int b = tid; b < B; b += 128) {
             const int L = __ldg(cache_len + b);
@@ -258,10 +266,10 @@ __global__ void __launch_bounds__(128) cache_attend_kernel(
     }
     const int64_t g0 = blockIdx.x * total / ctas;
     const int n_tiles = static_cast<int>((blockIdx.x + 1) * total / ctas - g0);
-    TilePos cur = cache_locate(cache_len, g0, B, Hk, T, s, k, lane);
+    TilePos cur = cache_locate(cache_len, g0, B, Hk, T, S, k, lane);
 
     if (tid == 0) {
-        for (int i = 0; i < 6; ++i) mbar_init(bars + i, 1);
+        for (int i = 0; i < 4; ++i) mbar_init(bars + i, 1);
         *abort_flag = 0;
         fence_barrier_init();
     }
@@ -269,8 +277,10 @@ __global__ void __launch_bounds__(128) cache_attend_kernel(
         tmem_alloc(tmem_slot, SM::kTmemCols);
         tmem_relinquish();
     }
+    // rows of heads past G stay zero: logits 0, nothing of them is written
     for (int e = tid; e < (SM::kNS + SM::kNP) * 8; e += 128)
         *reinterpret_cast<uint4 *>(smem + SM::kQ + e * 16) = make_uint4(0u, 0u, 0u, 0u);
+    if (tid < NH) head_f[tid] = 0.f, head_m[tid] = -INFINITY, head_l[tid] = 0.f;
     grid_dependency_wait();  // the selection (k > 0) has been written
     tc_fence_before();
     __syncthreads();
@@ -278,98 +288,98 @@ __global__ void __launch_bounds__(128) cache_attend_kernel(
     grid_dependents_launch();
     const uint32_t tmem = *tmem_slot;
 
-    const int per = 128 / s, seg = tid / s;  // blocks of a tile, this key's block among them
     struct Blocks {
-        int v[2];
+        int v[kPer];  // -1: none
     };
-    // blocks of a tile (-1: none); only positions that cache_locate and next() give are asked for
     auto blocks_of = [&](const TilePos &p) {
         Blocks r;
-        const int ns = cache_slots(p.L, T, s, k);
+        const int bt = p.L / S;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int slot = p.t * per + i;
-            r.v[i] = -1;
-            if (i < per && slot < ns)
-                r.v[i] = k > 0 ? __ldcg(idx + (static_cast<size_t>(p.b) * Hk + p.hk) * k + slot) : slot;
+        for (int i = 0; i < kPer; ++i) {
+            const int slot = p.t * kPer + i;
+            if (k > 0)
+                r.v[i] = slot < k ? __ldcg(idx + (static_cast<size_t>(p.b) * Hk + p.hk) * k + slot) : -1;
+            else
+                r.v[i] = slot;
+            if (r.v[i] > bt) r.v[i] = -1;
         }
         return r;
     };
-    auto usable = [&](int blk, int L) { return blk >= 0 && blk <= L / s; };
-    // (thread 0) keys or values of one tile into stage st
-    auto load = [&](const CUtensorMap *map, uint64_t *bar, int st, int off, const TilePos &p, const Blocks &r) {
+    // (one thread) the keys or values of one tile
+    auto load = [&](const CUtensorMap *map, uint64_t *bar, uint32_t off, const TilePos &p, const Blocks &r) {
         uint32_t bytes = 0;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            if (usable(r.v[i], p.L)) bytes += s * kCacheD;
-        mbar_arrive_expect_tx(bar + st, bytes);
+        for (int i = 0; i < kPer; ++i)
+            if (r.v[i] >= 0) bytes += S * kCacheD;
+        mbar_arrive_expect_tx(bar, bytes);
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            if (usable(r.v[i], p.L))  // (the host keeps B * Hkv * T below 2^31)
-                tma_load_2d(map, bar + st, smem + st * 2 * SM::kTile + off + i * s * kCacheD, 0,
-                            (p.b * Hk + p.hk) * T + r.v[i] * s);
+        for (int i = 0; i < kPer; ++i)
+            if (r.v[i] >= 0)  // (the host keeps B * Hkv * T below 2^31)
+                tma_load_2d(map, bar, smem + off + i * S * kCacheD, 0, (p.b * Hk + p.hk) * T + r.v[i] * S);
     };
     struct Scales {
-        float k, v, vmax;
+        float k, v, top;  // this key's block's; the largest value scale of the tile
     };
-    auto scales_of = [&](const TilePos &p, const Blocks &r) {  // of this thread's key's block
+    auto scales_of = [&](const TilePos &p, const Blocks &r) {
         const size_t at = (static_cast<size_t>(p.b) * Hk + p.hk) * nb;
         Scales c{0.f, 0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            if (usable(r.v[i], p.L)) {
+        for (int i = 0; i < kPer; ++i)
+            if (r.v[i] >= 0) {
                 const float v = __ldg(Vscale + at + r.v[i]);
-                c.vmax = fmaxf(c.vmax, v);
-                if (i == seg) c.v = v, c.k = __ldg(Kscale + at + r.v[i]);
+                c.top = fmaxf(c.top, v);
+                if (i == tid / S) c.v = v, c.k = __ldg(Kscale + at + r.v[i]);
             }
         return c;
     };
 
-    Blocks blk = blocks_of(cur), blk1{{-1, -1}}, blk2{{-1, -1}};
-    Scales sc = scales_of(cur, blk), sc1{0.f, 0.f, 0.f};
+    constexpr int kLoader = 96;  // the thread that issues the loads (thread 0 issues the products)
+    Blocks blk = blocks_of(cur), blk1 = blk, blk2 = blk;
+    int loads_k = 0, loads_v = 0, products_s = 0, products_o = 0;  // issued by this thread
+    if (tid == kLoader) {
+        load(&mapK, bar_k, 0, cur, blk);
+        load(&mapV, bar_v, SM::kTile, cur, blk);
+        loads_k = loads_v = 1;
+    }
+    Scales sc = scales_of(cur, blk), sc1 = sc;
     TilePos pos1 = cur, pos2;
     if (n_tiles > 1) {
-        pos1.next(cache_len, B, Hk, T, s, k);
+        pos1.next(cache_len, B, Hk, T, S, k);
         blk1 = blocks_of(pos1);
     }
     pos2 = pos1;
-    int loaded_k = 0, loaded_v = 0;  // (thread 0) tiles whose loads have been issued
-    if (tid == 0) {
-        load(&mapK, bar_k, 0, 0, cur, blk);
-        load(&mapV, bar_v, 0, SM::kTile, cur, blk);
-        loaded_k = loaded_v = 1;
-        if (n_tiles > 1) {
-            load(&mapK, bar_k, 1, 0, pos1, blk1);
-            load(&mapV, bar_v, 1, SM::kTile, pos1, blk1);
-            loaded_k = loaded_v = 2;
-        }
-    }
-    int issued_s = 0, issued_o = 0;  // (thread 0) products issued
     auto leave = [&](bool failed) {
-        if (failed && tid == 0) {  // let the loads and products in flight finish
-            for (int st = 0; st < SM::kStages; ++st) {
-                const int nk = (loaded_k - st + 1) / 2, nv = (loaded_v - st + 1) / 2;  // loads into this stage
-                if (nk > 0) mbar_drain(bar_k + st, (nk - 1) & 1);
-                if (nv > 0) mbar_drain(bar_v + st, (nv - 1) & 1);
-            }
-            if (issued_s) mbar_drain(bar_s, (issued_s - 1) & 1);
-            if (issued_o) mbar_drain(bar_o, (issued_o - 1) & 1);
+        if (failed) {  // let the loads and products in flight finish
+            if (loads_k) mbar_drain(bar_k, (loads_k - 1) & 1);
+            if (loads_v) mbar_drain(bar_v, (loads_v - 1) & 1);
+            if (products_s) mbar_drain(bar_s, (products_s - 1) & 1);
+            if (products_o) mbar_drain(bar_o, (products_o - 1) & 1);
         }
         tc_fence_before();
         __syncthreads();
         tc_fence_after();
         if (warp == 1) tmem_dealloc(tmem, SM::kTmemCols);
     };
+    auto product_s = [&]() {  // (thread 0) the keys have landed
+        tc_fence_after();
+        constexpr uint32_t id = idesc_e4m3(128, SM::kNS, false, false);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+            mma_e4m3_ss(tmem, smem_desc_sw128(sK + kk * 32, 16), smem_desc_sw128(sQ + kk * 32, 16), id, kk > 0 ? 1u : 0u);
+        mma_commit(bar_s);
+        ++products_s;
+    };
 
     float o[NH];
     int pair = -1;
     for (int it = 0; it < n_tiles; ++it) {
-        const int st = it & 1, ph = (it >> 1) & 1;
+        const uint32_t ph = it & 1;
         const int bh = cur.b * Hk + cur.hk;
+        const bool last = it + 1 == n_tiles || pos1.b * Hk + pos1.hk != bh;  // of this pair
         // the next tile's scales and the one after's blocks arrive during this tile
         if (it + 1 < n_tiles) sc1 = scales_of(pos1, blk1);
         if (it + 2 < n_tiles) {
-            pos2.next(cache_len, B, Hk, T, s, k);
+            pos2.next(cache_len, B, Hk, T, S, k);
             blk2 = blocks_of(pos2);
         }
         if (bh != pair) {  // a new group of query heads: two terms per element, two rows per head
@@ -409,81 +419,71 @@ __global__ void __launch_bounds__(128) cache_attend_kernel(
             __syncthreads();
         }
         bool ok = true;
-        if (tid == 0) {
-            ok = mbar_wait(bar_k + st, ph, abort_flag, 0x711);
-            if (ok) {
-                tc_fence_after();
-                const uint32_t a = smem_u32(smem + st * 2 * SM::kTile);
-                constexpr uint32_t id = idesc_e4m3(128, SM::kNS, false, false);
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    mma_e4m3_ss(tmem, smem_desc_sw128(a + kk * 32, 16), smem_desc_sw128(sQ + kk * 32, 16), id,
-                                kk > 0 ? 1u : 0u);
-                mma_commit(bar_s);
-                ++issued_s;
-            }
+        if (tid == 0 && products_s == it) {
+            ok = mbar_wait(bar_k, ph, abort_flag, 0x711);
+            if (ok) product_s();
         }
-        ok = ok && mbar_wait(bar_s, it & 1, abort_flag, 0x712);
-        if (__syncthreads_or(!ok)) {
-            leave(true);
-            return;
-        }
+        ok = ok && mbar_wait(bar_s, ph, abort_flag, 0x712);
         tc_fence_after();
-        if (tid == 0 && it + 2 < n_tiles) {  // the keys have been read
-            load(&mapK, bar_k, st, 0, pos2, blk2);
-            ++loaded_k;
+        if (tid == kLoader && ok && it + 1 < n_tiles) {  // the keys have been read
+            load(&mapK, bar_k, 0, pos1, blk1);
+            ++loads_k;
         }
-        const int my_blk = seg ? blk.v[1] : blk.v[0];
-        const bool valid = usable(my_blk, cur.L) && my_blk * s + tid % s <= cur.L;
+        const int my_blk = kPer == 1 ? blk.v[0] : (tid < S ? blk.v[0] : blk.v[kPer - 1]);
+        const bool valid = my_blk >= 0 && my_blk * S + tid % S <= cur.L;
+        float *red_m = reinterpret_cast<float *>(smem + SM::kRed + (it & 1) * 2 * NH * 16), *red_l = red_m + NH * 4;
         float p[NH];
         {
             const uint32_t row = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-            if constexpr (NH == 8) {
+            if constexpr (NH <= 8) {
                 float v[16];
                 tmem_ld16(row, v);
 #pragma unroll
-                for (int h = 0; h < 8; ++h) p[h] = fmaf(v[8 + h], 0.0625f, v[h]);
+                for (int h = 0; h < NH; ++h) p[h] = fmaf(v[NH + h], 0.0625f, v[h]);
             } else if constexpr (NH == 16) {
                 float v[32];
                 tmem_ld32(row, v);
 #pragma unroll
                 for (int h = 0; h < 16; ++h) p[h] = fmaf(v[16 + h], 0.0625f, v[h]);
             } else {
-                float v[32], w[32];
-                tmem_ld32(row, v);
-                tmem_ld32(row + 32, w);
+                float v[32];
+                tmem_ld32(row, p);
+                tmem_ld32(row + 32, v);
 #pragma unroll
-                for (int h = 0; h < 32; ++h) p[h] = fmaf(w[h], 0.0625f, v[h]);
+                for (int h = 0; h < 32; ++h) p[h] = fmaf(v[h], 0.0625f, p[h]);
             }
         }
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
-            if (h < G) {
-                p[h] = valid ? p[h] * (sc.k * head_f[h]) : -INFINITY;
-                float m;
-                asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(p[h]));
-                if (lane == 0) red_m[h * 4 + warp] = m;
-            }
+            p[h] = valid ? p[h] * (sc.k * head_f[h]) : -INFINITY;
+            float m;
+            asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(p[h]));
+            if (lane == 0) red_m[h * 4 + warp] = m;
         }
+        tc_fence_before();
         __syncthreads();
-        // weights against the new maximum; the outputs so far are brought to it below
-        float vs = sc.v;
-        const float vtop = sc.vmax;
-        vs = vtop > 0.f ? vs / vtop : 0.f;  // both powers of two
-        float sum[NH], shrink[NH];
+        // weights against the new maximum, in units of 1/256 of the tile's largest value scale
+        float sum[NH];
+        bool grown = false;
+        const float unit = kPer == 1 ? 256.f : (sc.top > 0.f ? 256.f * (sc.v / sc.top) : 0.f);  // powers of two
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
-            sum[h] = 0.f;
-            shrink[h] = 1.f;
-            if (h < G) {
+            const float4 r = *reinterpret_cast<const float4 *>(red_m + h * 4);
+            const float old = head_m[h];
+            float m = fmaxf(fmaxf(fmaxf(r.x, r.y), fmaxf(r.z, r.w)), old);
+            if (m == -INFINITY) m = 0.f;  // only overflowing logits: weights 0
+            grown |= m != old;
+            sum[h] = fast_exp2(p[h] - m);  // 0 for a masked key
+            p[h] = sum[h] * unit;
+        }
+        if (grown) {  // (uniform) the outputs so far are brought to the new maxima
+#pragma unroll
+            for (int h = 0; h < NH; ++h) {
                 const float4 r = *reinterpret_cast<const float4 *>(red_m + h * 4);
                 const float old = head_m[h];
                 float m = fmaxf(fmaxf(fmaxf(r.x, r.y), fmaxf(r.z, r.w)), old);
-                if (m == -INFINITY) m = 0.f;  // only overflowing logits: weights 0
-                if (m != old) shrink[h] = fast_exp2(old - m);
-                p[h] = valid ? fast_exp2(p[h] - m) : 0.f;
-                sum[h] = p[h];
-                p[h] *= 256.f * vs;
+                if (m == -INFINITY) m = 0.f;
+                o[h] *= m != old ? fast_exp2(old - m) : 1.f;
             }
         }
         // sums over the warp: each step hands a lane half of the heads it holds
@@ -503,8 +503,7 @@ __global__ void __launch_bounds__(128) cache_attend_kernel(
 #pragma unroll
             for (; off >= 1; off >>= 1) sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], off);
             constexpr int kLanes = 32 / NH;  // lanes that end up with the same head
-            const int h = lane / kLanes;
-            if (lane % kLanes == 0 && h < G) red_l[h * 4 + warp] = sum[0];
+            if (lane % kLanes == 0) red_l[lane / kLanes * 4 + warp] = sum[0];
         }
         // three terms of every weight into the K-major operand: row term * NH + h, byte = key
         {
@@ -515,13 +514,13 @@ __global__ void __launch_bounds__(128) cache_attend_kernel(
             };
 #pragma unroll
             for (int h = 0; h < NH; h += 2) {
-                if (h < G) {
-                    float a = p[h], c = p[h + 1];
+                float a = p[h], c = p[h + 1];
 #pragma unroll
-                    for (int term = 0; term < 3; ++term) {
-                        const uint16_t w = pack_e4m3x2(a, c);
-                        put(term * NH + h, w & 0xFFu);
-                        put(term * NH + h + 1, w >> 8);
+                for (int term = 0; term < 3; ++term) {
+                    const uint16_t w = pack_e4m3x2(a, c);
+                    put(term * NH + h, w & 0xFFu);
+                    put(term * NH + h + 1, w >> 8);
+                    if (term < 2) {
                         const float2 f = unpack_e4m3x2(w);
                         a = (a - f.x) * 16.f;
                         c = (c - f.y) * 16.f;
@@ -529,9 +528,9 @@ __global__ void __launch_bounds__(128) cache_attend_kernel(
                 }
             }
         }
-        ok = mbar_wait(bar_v + st, ph, abort_flag, 0x713);
+        ok = ok && mbar_wait(bar_v, ph, abort_flag, 0x713);
         if (ok && !valid) {  // whatever the cache holds behind the newest token must not meet even a weight of 0
-            uint4 *row = reinterpret_cast<uint4 *>(smem + st * 2 * SM::kTile + SM::kTile + tid * kCacheD);
+            uint4 *row = reinterpret_cast<uint4 *>(smem + SM::kTile + tid * kCacheD);
 #pragma unroll
             for (int i = 0; i < 8; ++i) row[i] = make_uint4(0u, 0u, 0u, 0u);
         }
@@ -543,17 +542,18 @@ __global__ void __launch_bounds__(128) cache_attend_kernel(
         }
         if (tid == 0) {
             tc_fence_after();
-            const uint32_t a = smem_u32(smem + st * 2 * SM::kTile + SM::kTile);
             constexpr uint32_t id = idesc_e4m3(128, SM::kNP, true, false);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-                mma_e4m3_ss(tmem + SM::kTmemO, smem_desc_sw128(a + kk * 4096, 16), smem_desc_sw128(sP + kk * 32, 16),
+                mma_e4m3_ss(tmem + SM::kTmemO, smem_desc_sw128(sV + kk * 4096, 16), smem_desc_sw128(sP + kk * 32, 16),
                             id, kk > 0 ? 1u : 0u);
             mma_commit(bar_o);
-            ++issued_o;
+            ++products_o;
+            // the next tile's logits follow at once where its keys are there and the query heads are the same
+            if (SM::kApart && !last && mbar_test_wait(bar_k, ph ^ 1)) product_s();
         }
         // meanwhile: the head's running maximum and sum, and the blocks' own
-        if (tid < G) {
+        if (tid < NH) {
             const float4 rm = *reinterpret_cast<const float4 *>(red_m + tid * 4);
             const float4 rl = *reinterpret_cast<const float4 *>(red_l + tid * 4);
             const float old = head_m[tid];
@@ -562,49 +562,46 @@ __global__ void __launch_bounds__(128) cache_attend_kernel(
             const float l = (rl.x + rl.y) + (rl.z + rl.w);
             head_l[tid] = head_l[tid] * (m != old ? fast_exp2(old - m) : 1.f) + l;
             head_m[tid] = m;
-            if (block_ml) {
-                const size_t at = (static_cast<size_t>(bh) * G + tid) * (k > 0 ? k : nb) + cur.t * per;
-                if (s == 128) {
-                    block_ml[at] = make_float2(m, l);
+            if (block_ml && tid < G) {
+                float2 *to = block_ml + (static_cast<size_t>(bh) * G + tid) * (k > 0 ? k : nb) + cur.t * kPer;
+                if (kPer == 1) {
+                    to[0] = make_float2(m, l);
                 } else {
-                    block_ml[at] = make_float2(m, rl.x + rl.y);
-                    if (blk.v[1] >= 0) block_ml[at + 1] = make_float2(m, rl.z + rl.w);
+                    to[0] = make_float2(m, rl.x + rl.y);
+                    if (blk.v[kPer - 1] >= 0) to[1] = make_float2(m, rl.z + rl.w);
                 }
             }
         }
-        ok = mbar_wait(bar_o, it & 1, abort_flag, 0x714);
-        if (__syncthreads_or(!ok)) {
-            leave(true);
-            return;
-        }
+        ok = mbar_wait(bar_o, ph, abort_flag, 0x714);  // (a failure is met at the next tile's barrier, or below)
         tc_fence_after();
-        if (tid == 0 && it + 2 < n_tiles) {  // the values have been read
-            load(&mapV, bar_v, st, SM::kTile, pos2, blk2);
-            ++loaded_v;
+        if (tid == kLoader && ok && it + 1 < n_tiles) {  // the values have been read
+            load(&mapV, bar_v, SM::kTile, pos1, blk1);
+            ++loads_v;
         }
         {
             const uint32_t row = tmem + SM::kTmemO + (static_cast<uint32_t>(warp * 32) << 16);
-            const float unit = vtop * (1.f / 256.f);
-            if constexpr (NH == 8) {
+            const float back = sc.top * (1.f / 256.f);
+            if constexpr (NH == 4) {
+                float v[16];
+                tmem_ld16(row, v);
+#pragma unroll
+                for (int h = 0; h < 4; ++h) o[h] = fmaf(fmaf(fmaf(v[8 + h], 0.0625f, v[4 + h]), 0.0625f, v[h]), back, o[h]);
+            } else if constexpr (NH == 8) {
                 float v[32];
                 tmem_ld32(row, v);
 #pragma unroll
-                for (int h = 0; h < 8; ++h)
-                    o[h] = fmaf(fmaf(fmaf(v[16 + h], 0.0625f, v[8 + h]), 0.0625f, v[h]), unit, o[h] * shrink[h]);
+                for (int h = 0; h < 8; ++h) o[h] = fmaf(fmaf(fmaf(v[16 + h], 0.0625f, v[8 + h]), 0.0625f, v[h]), back, o[h]);
             } else if constexpr (NH == 16) {
                 float v[32], w[16];
                 tmem_ld32(row, v);
                 tmem_ld16(row + 32, w);
 #pragma unroll
-                for (int h = 0; h < 16; ++h)
-                    o[h] = fmaf(fmaf(fmaf(w[h], 0.0625f, v[16 + h]), 0.0625f, v[h]), unit, o[h] * shrink[h]);
+                for (int h = 0; h < 16; ++h) o[h] = fmaf(fmaf(fmaf(w[h], 0.0625f, v[16 + h]), 0.0625f, v[h]), back, o[h]);
             } else {
-                float v[32];
-#pragma unroll
-                for (int h = 0; h < 32; ++h) o[h] *= shrink[h];
-                float f = unit;
+                float f = back;
 #pragma unroll
                 for (int term = 0; term < 3; ++term, f *= 0.0625f) {
+                    float v[32];
                     tmem_ld32(row + 32 * term, v);
 #pragma unroll
                     for (int h = 0; h < 32; ++h) o[h] = fmaf(v[h], f, o[h]);
@@ -612,8 +609,11 @@ __global__ void __launch_bounds__(128) cache_attend_kernel(
             }
             tc_fence_before();
         }
-        const bool last = it + 1 == n_tiles || pos1.b * Hk + pos1.hk != bh;
         if (last) {
+            if (__syncthreads_or(!ok)) {  // (also: head_m and head_l are complete)
+                leave(true);
+                return;
+            }
             const size_t slot = static_cast<size_t>(blockIdx.x) + bh;
             float *to = opart + slot * G * kCacheD + tid;
 #pragma unroll
@@ -621,6 +621,8 @@ __global__ void __launch_bounds__(128) cache_attend_kernel(
                 if (h < G) to[h * kCacheD] = o[h];
             if (tid < G) mlpart[slot * G + tid] = make_float2(head_m[tid], head_l[tid]);
             __syncthreads();  // head_* are set anew for the next pair
+        } else if (!SM::kApart) {
+            __syncthreads();  // every warp has read its outputs before the next logits take their place
         }
         cur = pos1;
         pos1 = pos2;

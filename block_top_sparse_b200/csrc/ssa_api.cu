@@ -8,6 +8,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <type_traits>
 
 #include "ssa.h"
 
@@ -112,8 +113,14 @@ ssa_status_t check_cache_dims(const ssa_dims_t *dims, Shape &S) {
 
 // Query heads per key head padded to a kernel's, and the grid of cache_attend_kernel: the CTAs that its shared
 // memory lets reside at once.
-inline int cache_heads(int G) { return G <= 8 ? 8 : G <= 16 ? 16 : 32; }
-inline unsigned cache_grid(int G) { return kCacheSms * (G <= 8 ? 3u : 2u); }
+inline int cache_heads(int G) { return G <= 4 ? 4 : G <= 8 ? 8 : G <= 16 ? 16 : 32; }
+inline unsigned cache_grid(int G) {
+    const int NH = cache_heads(G);
+    return kCacheSms * (NH == 4   ? CacheAttend<4>::kPerSm
+                        : NH == 8 ? CacheAttend<8>::kPerSm
+                        : NH == 16 ? CacheAttend<16>::kPerSm
+                                   : CacheAttend<32>::kPerSm);
+}
 
 inline size_t align_up(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
@@ -987,15 +994,21 @@ ssa_status_t ssa_cache_decode(const ssa_dims_t *dims, const int32_t *cache_len, 
         const float scale_log2 = static_cast<float>(S.scale * 1.4426950408889634);
         if (S.k > 0)
             return launch_dependent(kernel, grid, 128, smem, st, tmK, tmV, cache_len, qb, Kscale, Vscale, idx, opart, ml,
-                                    block_ml, S.B, S.Hk, S.G, S.T, S.s, S.k, S.nb, scale_log2);
+                                    block_ml, S.B, S.Hk, S.G, S.T, S.k, S.nb, scale_log2);
         kernel<<<grid, 128, smem, st>>>(tmK, tmV, cache_len, qb, Kscale, Vscale, idx, opart, ml, block_ml, S.B, S.Hk, S.G,
-                                        S.T, S.s, S.k, S.nb, scale_log2);
+                                        S.T, S.k, S.nb, scale_log2);
         return true;
     };
+    auto heads = [&](auto nh) {
+        constexpr int NH = decltype(nh)::value;
+        return S.s == 128 ? attend(cache_attend_kernel<NH, 128>, CacheAttend<NH>::kBytes)
+                          : attend(cache_attend_kernel<NH, 64>, CacheAttend<NH>::kBytes);
+    };
     const int NH = cache_heads(S.G);
-    const bool ok = NH == 8    ? attend(cache_attend_kernel<8>, CacheAttendSmem<8>::kTotal)
-                    : NH == 16 ? attend(cache_attend_kernel<16>, CacheAttendSmem<16>::kTotal)
-                               : attend(cache_attend_kernel<32>, CacheAttendSmem<32>::kTotal);
+    const bool ok = NH == 4    ? heads(std::integral_constant<int, 4>())
+                    : NH == 8  ? heads(std::integral_constant<int, 8>())
+                    : NH == 16 ? heads(std::integral_constant<int, 16>())
+                               : heads(std::integral_constant<int, 32>());
     if (!ok) return SSA_ERR_CUDA;
     if (!launch_dependent(cache_combine_kernel, dim3(bhk), 256, 0, st, cache_len, opart, ml, block_ml, idx,
                           static_cast<__nv_bfloat16 *>(o), lse, weight_in, weight_out, S.B, S.Hk, S.G, S.T, S.s, S.k, S.nb,
