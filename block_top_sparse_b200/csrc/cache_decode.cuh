@@ -27,9 +27,8 @@
 //                          pairs, so long and short sequences balance, and
 //                          writes an unnormalised partial output, maximum and
 //                          sum for each pair that it touches;
-//   cache_combine_kernel   one CTA per (sequence, key head): joins the partials
-//                          in a fixed order; block weights from the blocks' own
-//                          maxima and sums.
+//   cache_combine_kernel   joins a pair's partials in a fixed order; block weights
+//                          from the blocks' own maxima and sums.
 // No atomics: results are the same from run to run.
 #pragma once
 
@@ -67,8 +66,17 @@ __global__ void __launch_bounds__(kTopThreads) cache_select_kernel(const int32_t
     __shared__ double qs[kCacheD];
     grid_dependents_launch();
     const int bh = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    constexpr int R = 8, kWarps = kTopThreads / 32;  // rows in flight per warp
     const int L = __ldg(cache_len + bh / Hk);
     int32_t *out = idx + static_cast<size_t>(bh) * k;
+    float4 v[R];
+    const float4 *kb = reinterpret_cast<const float4 *>(Kbar + static_cast<size_t>(bh) * nb * kCacheD) + lane;
+    auto load = [&](int j0, int n) {
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            v[i] = j0 + i < n ? __ldg(kb + static_cast<size_t>(j0 + i) * (kCacheD / 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    if (k > 1) load(R * warp, nb);  // before the length is known: the first rows, whether they count or not
     if (L < 0 || L >= T) {
         for (int i = tid; i < k; i += kTopThreads) out[i] = -1;
         return;
@@ -86,20 +94,14 @@ __global__ void __launch_bounds__(kTopThreads) cache_select_kernel(const int32_t
             double q4[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) q4[i] = qs[4 * lane + i];
-            constexpr int R = 8;  // rows in flight per warp
-            const float4 *kb = reinterpret_cast<const float4 *>(Kbar + static_cast<size_t>(bh) * nb * kCacheD) + lane;
-            for (int j0 = R * warp; j0 < bt; j0 += R * (kTopThreads / 32)) {
-                float4 v[R];
-#pragma unroll
-                for (int i = 0; i < R; ++i)
-                    v[i] = j0 + i < bt ? __ldg(kb + static_cast<size_t>(j0 + i) * (kCacheD / 4))
-                                       : make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int j0 = R * warp; j0 < bt; j0 += R * kWarps) {
                 double part[R];
 #pragma unroll
                 for (int i = 0; i < R; ++i)
                     part[i] = fma(q4[0], static_cast<double>(v[i].x),
                                   fma(q4[1], static_cast<double>(v[i].y),
                                       fma(q4[2], static_cast<double>(v[i].z), q4[3] * static_cast<double>(v[i].w))));
+                load(j0 + R * kWarps, bt);  // the next rows arrive during the sums
                 // butterfly: three steps hand each lane the sum of one row over 8 lanes, two more the whole sum
 #pragma unroll
                 for (int off = 16, n = R / 2; n >= 1; off >>= 1, n >>= 1) {
@@ -634,104 +636,123 @@ __global__ void __launch_bounds__(128, CacheAttend<NH>::kPerSm) cache_attend_ker
 }
 
 // ---------------------------------------------------------------------------
-// Joining the partials: M = max m_i, o = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i, in the order of the CTAs.
+// Joining the partials: M = max m_i, l = sum 2^(m_i - M) l_i, o = sum 2^(m_i - M) o_i / l, in the order of the
+// CTAs.  grid (B * Hk, head CTAs + weight CTAs): a head CTA joins 8 / WPH query heads, WPH warps each; a weight
+// CTA adds up the attention weight of 256 blocks over the group's heads.  WPH = 8 where a pair is split over
+// many CTAs (few sequences), 1 where there are many pairs of few partials.
 // ---------------------------------------------------------------------------
+struct CachePartials {
+    int n;
+    size_t slot0;
+};
+
+// The CTAs c with tiles of a pair: c * total / ctas <= tile < (c + 1) * total / ctas.
+__device__ __forceinline__ CachePartials cache_partials_of(int64_t total, int64_t first, int nt, int grid, int bh) {
+    const int64_t ctas = min(static_cast<int64_t>(grid), total);
+    const int c0 = static_cast<int>(((first + 1) * ctas - 1) / total);
+    const int c1 = static_cast<int>(((first + nt) * ctas - 1) / total);
+    return CachePartials{c1 - c0 + 1, static_cast<size_t>(c0) + bh};
+}
+
+// Maximum and sum of one head, by one warp.
+__device__ __forceinline__ float2 cache_join(const float2 *ml, int n, int G, int h, int lane) {
+    float m = -INFINITY, l = 0.f;
+    for (int i = lane; i < n; i += 32) {
+        const float2 a = __ldcg(ml + static_cast<size_t>(i) * G + h);
+        const float top = fmaxf(m, a.x);
+        l = l * (m == top ? 1.f : fast_exp2(m - top)) + a.y * (a.x == top ? 1.f : fast_exp2(a.x - top));
+        m = top;
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        const float m2 = __shfl_xor_sync(0xffffffffu, m, off), l2 = __shfl_xor_sync(0xffffffffu, l, off);
+        const float top = fmaxf(m, m2);
+        l = l * (m == top ? 1.f : fast_exp2(m - top)) + l2 * (m2 == top ? 1.f : fast_exp2(m2 - top));
+        m = top;
+    }
+    return make_float2(m, l);
+}
+
+template <int WPH>
 __global__ void __launch_bounds__(256) cache_combine_kernel(const int32_t *__restrict__ cache_len,
                                                             const float *opart, const float2 *mlpart,
                                                             const float2 *block_ml, const int32_t *idx,
                                                             __nv_bfloat16 *__restrict__ o, float *__restrict__ lse,
                                                             const float *weight_in, float *weight_out, int B, int Hk,
                                                             int G, int T, int s, int k, int nb, int grid) {
-    __shared__ float head_m[kCacheMaxGroup], head_l[kCacheMaxGroup];
+    constexpr int kHeads = 8 / WPH;  // per head CTA
+    __shared__ float2 head[kCacheMaxGroup];
     __shared__ float4 part[8][32];
     const int bh = blockIdx.x, b = bh / Hk, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int L = __ldg(cache_len + b), nt = cache_tiles(L, T, s, k), ns = cache_slots(L, T, s, k);
     const int64_t total = cache_total_tiles(cache_len, B, Hk, T, s, k, lane);
     const int64_t first = cache_tiles_before(cache_len, b, T, s, k, lane) * Hk + static_cast<int64_t>(bh % Hk) * nt;
+    const int head_ctas = (G + kHeads - 1) / kHeads;
     grid_dependency_wait();
-    if (nt == 0) {  // no token (or a bad length): empty attention
-        for (int e = tid; e < G * kCacheD; e += 256) o[static_cast<size_t>(bh) * G * kCacheD + e] = __float2bfloat16_rn(0.f);
-        if (tid < G) lse[static_cast<size_t>(bh) * G + tid] = -INFINITY;
-        if (weight_out)
-            for (int j = tid; j < nb; j += 256)
-                weight_out[static_cast<size_t>(bh) * nb + j] = weight_in ? weight_in[static_cast<size_t>(bh) * nb + j] : 0.f;
-        return;
-    }
-    // CTAs c with tiles of this pair: c * total / ctas <= tile < (c + 1) * total / ctas
-    const int64_t ctas = min(static_cast<int64_t>(grid), total);
-    const int c0 = static_cast<int>(((first + 1) * ctas - 1) / total);
-    const int c1 = static_cast<int>(((first + nt) * ctas - 1) / total);
-    const int np = c1 - c0 + 1;
-    const size_t slot0 = static_cast<size_t>(c0) + bh;
-    const float2 *ml = mlpart + slot0 * G;
-    for (int h = warp; h < G; h += 8) {
-        float m = -INFINITY, l = 0.f;
-        for (int i = lane; i < np; i += 32) m = fmaxf(m, __ldcg(ml + static_cast<size_t>(i) * G + h).x);
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-        for (int i = lane; i < np; i += 32) {
-            const float2 a = __ldcg(ml + static_cast<size_t>(i) * G + h);
-            l += a.y * fast_exp2(a.x - m);
-        }
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
-        if (lane == 0) {
-            head_m[h] = m;
-            head_l[h] = l;
-            lse[static_cast<size_t>(bh) * G + h] = fmaf(m, kLn2, logf(l));
-        }
-    }
-    __syncthreads();
-    // outputs: a warp per head (G >= 8), or several warps per head that take every ng-th partial
-    const int ng = G >= 8 ? 1 : 8 / G;
-    for (int h0 = 0; h0 < G; h0 += 8) {
-        const int h = G >= 8 ? h0 + warp : warp % G, grp = G >= 8 ? 0 : warp / G;
+    CachePartials P{0, 0};
+    if (nt > 0) P = cache_partials_of(total, first, nt, grid, bh);
+    const float2 *ml = mlpart + P.slot0 * G;
+    if (static_cast<int>(blockIdx.y) < head_ctas) {
+        const int h = blockIdx.y * kHeads + warp / WPH, grp = warp % WPH;
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (h < G && grp < ng) {
-            const float m = head_m[h];
-            const float4 *op = reinterpret_cast<const float4 *>(opart + (slot0 * G + h) * kCacheD) + lane;
+        float2 t = make_float2(-INFINITY, 0.f);
+        if (h < G && nt > 0) {
+            t = cache_join(ml, P.n, G, h, lane);
+            const float4 *op = reinterpret_cast<const float4 *>(opart + (P.slot0 * G + h) * kCacheD) + lane;
 #pragma unroll 8
-            for (int i = grp; i < np; i += ng) {
-                const float f = fast_exp2(__ldcg(ml + static_cast<size_t>(i) * G + h).x - m);
+            for (int i = grp; i < P.n; i += WPH) {
+                const float f = fast_exp2(__ldcg(ml + static_cast<size_t>(i) * G + h).x - t.x);
                 const float4 v = __ldcg(op + static_cast<size_t>(i) * G * (kCacheD / 4));
                 a.x = fmaf(f, v.x, a.x), a.y = fmaf(f, v.y, a.y), a.z = fmaf(f, v.z, a.z), a.w = fmaf(f, v.w, a.w);
             }
         }
-        if (ng > 1) {
+        if (WPH > 1) {
             part[warp][lane] = a;
             __syncthreads();
             if (grp == 0)
-                for (int i = 1; i < ng; ++i) {
-                    const float4 v = part[warp + i * G][lane];
+#pragma unroll
+                for (int i = 1; i < WPH; ++i) {
+                    const float4 v = part[warp + i][lane];
                     a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
                 }
         }
         if (h < G && grp == 0) {
-            const float inv = 1.f / head_l[h];
-            reinterpret_cast<uint2 *>(o + (static_cast<size_t>(bh) * G + h) * kCacheD)[lane] =
+            const float inv = nt > 0 ? 1.f / t.y : 0.f;  // no token (or a bad length): o = 0
+            const size_t row = static_cast<size_t>(bh) * G + h;
+            reinterpret_cast<uint2 *>(o + row * kCacheD)[lane] =
                 make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+            if (lane == 0) lse[row] = nt > 0 ? fmaf(t.x, kLn2, logf(t.y)) : -INFINITY;
         }
+        return;
     }
-    if (!weight_out) return;
-    const float *win = weight_in ? weight_in + static_cast<size_t>(bh) * nb : nullptr;
-    float *wout = weight_out + static_cast<size_t>(bh) * nb;
-    auto mass = [&](int slot, int slots) {  // attention weight of one attended block, over the group's heads
+    // attention weight of blocks [j0, j0 + 256)
+    const int j0 = (blockIdx.y - head_ctas) * 256, j = j0 + tid;
+    if (nt > 0) {
+        for (int h = warp; h < G; h += 8) {
+            const float2 t = cache_join(ml, P.n, G, h, lane);
+            if (lane == 0) head[h] = t;
+        }
+        __syncthreads();
+    }
+    auto mass = [&](int slot, int slots) {  // of one attended block
         float w = 0.f;
         const float2 *bl = block_ml + static_cast<size_t>(bh) * G * slots + slot;
+#pragma unroll 4
         for (int h = 0; h < G; ++h) {
             const float2 a = __ldcg(bl + static_cast<size_t>(h) * slots);
-            w += a.y * fast_exp2(a.x - head_m[h]) / head_l[h];
+            w += a.y * fast_exp2(a.x - head[h].x) / head[h].y;
         }
         return w;
     };
+    const size_t at = static_cast<size_t>(bh) * nb + j;
     if (k == 0) {
-        for (int j = tid; j < nb; j += 256) wout[j] = (win ? win[j] : 0.f) + (j < ns ? mass(j, nb) : 0.f);
+        if (j < nb) weight_out[at] = (weight_in ? weight_in[at] : 0.f) + (j < ns ? mass(j, nb) : 0.f);
     } else {
-        for (int j = tid; j < nb; j += 256) wout[j] = win ? win[j] : 0.f;
+        if (j < nb) weight_out[at] = weight_in ? weight_in[at] : 0.f;
         __syncthreads();
         for (int i = tid; i < ns; i += 256) {  // attended blocks are distinct
-            const int j = __ldcg(idx + static_cast<size_t>(bh) * k + i);
-            if (j >= 0 && j < nb) wout[j] += mass(i, k);
+            const int jj = __ldcg(idx + static_cast<size_t>(bh) * k + i);
+            if (jj >= j0 && jj < min(j0 + 256, nb)) weight_out[static_cast<size_t>(bh) * nb + jj] += mass(i, k);
         }
     }
 }
