@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kTopThreads) cache_evict_select_kernel(
     __syncthreads();
     const int left = min(whole, keep), used = left + begun;
     if (whole > keep) {
-        top_ascending(key, whole, keep, list, sc);
+        top_blocks(key, whole, keep, list, sc);
     } else {
         for (int r = tid; r < left; r += kTopThreads) list[r] = r;
     }

@@ -56,7 +56,7 @@ __device__ __forceinline__ int cache_tiles(int L, int T, int s, int k) {
 // Selection
 // ---------------------------------------------------------------------------
 // Shared memory: nb keys.  k >= 1.
-__global__ void __launch_bounds__(kTopThreads) cache_select_kernel(const int32_t *__restrict__ cache_len,
+__global__ void __launch_bounds__(kTopThreads, 4) cache_select_kernel(const int32_t *__restrict__ cache_len,
                                                                    const __nv_bfloat16 *__restrict__ q,
                                                                    const float *__restrict__ Kbar,
                                                                    int32_t *__restrict__ idx, int Hk, int G, int T,
@@ -66,45 +66,52 @@ __global__ void __launch_bounds__(kTopThreads) cache_select_kernel(const int32_t
     __shared__ double qs[kCacheD];
     grid_dependents_launch();
     const int bh = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    constexpr int R = 8, kWarps = kTopThreads / 32;  // rows in flight per warp
+    constexpr int R = 8, kWarps = kTopThreads / 32;  // rows in flight per warp, four elements per lane
     const int L = __ldg(cache_len + bh / Hk);
     int32_t *out = idx + static_cast<size_t>(bh) * k;
+    // the first rows (whether they count or not) and the query are asked for before the length is known
     float4 v[R];
     const float4 *kb = reinterpret_cast<const float4 *>(Kbar + static_cast<size_t>(bh) * nb * kCacheD) + lane;
-    auto load = [&](int j0, int n) {
-#pragma unroll
-        for (int i = 0; i < R; ++i)
-            v[i] = j0 + i < n ? __ldg(kb + static_cast<size_t>(j0 + i) * (kCacheD / 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    auto load = [&](int i, int j, int n) {
+        v[i] = j < n ? __ldg(kb + static_cast<size_t>(j) * (kCacheD / 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
     };
-    if (k > 1) load(R * warp, nb);  // before the length is known: the first rows, whether they count or not
+    if (k > 1) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) load(i, R * warp + i, nb);
+        if (tid < kCacheD) {
+            double sum = 0.0;
+            const __nv_bfloat16 *qr = q + static_cast<size_t>(bh) * G * kCacheD + tid;
+#pragma unroll 4
+            for (int h = 0; h < G; ++h) sum += static_cast<double>(__bfloat162float(qr[h * kCacheD]));
+            qs[tid] = sum;
+        }
+    }
     if (L < 0 || L >= T) {
         for (int i = tid; i < k; i += kTopThreads) out[i] = -1;
         return;
     }
     const int bt = L / s, want = min(k - 1, bt);
-    if (want < bt) {
-        if (want > 0) {
-            if (tid < kCacheD) {
-                double v = 0.0;
-                for (int h = 0; h < G; ++h)
-                    v += static_cast<double>(__bfloat162float(q[(static_cast<size_t>(bh) * G + h) * kCacheD + tid]));
-                qs[tid] = v;
-            }
-            __syncthreads();
-            double q4[4];
+    if (want == bt) {
+        for (int i = tid; i < want; i += kTopThreads) out[i] = i;
+    } else if (want > 0) {
+        __syncthreads();
+        double q4[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) q4[i] = qs[4 * lane + i];
-            for (int j0 = R * warp; j0 < bt; j0 += R * kWarps) {
-                double part[R];
+        for (int i = 0; i < 4; ++i) q4[i] = qs[4 * lane + i];
+        for (int j0 = R * warp; j0 < bt; j0 += R * kWarps) {
 #pragma unroll
-                for (int i = 0; i < R; ++i)
-                    part[i] = fma(q4[0], static_cast<double>(v[i].x),
-                                  fma(q4[1], static_cast<double>(v[i].y),
-                                      fma(q4[2], static_cast<double>(v[i].z), q4[3] * static_cast<double>(v[i].w))));
-                load(j0 + R * kWarps, bt);  // the next rows arrive during the sums
-                // butterfly: three steps hand each lane the sum of one row over 8 lanes, two more the whole sum
+            for (int half = 0; half < R; half += 4) {
+                double part[4];
 #pragma unroll
-                for (int off = 16, n = R / 2; n >= 1; off >>= 1, n >>= 1) {
+                for (int i = 0; i < 4; ++i) {
+                    const float4 x = v[half + i];
+                    part[i] = fma(q4[0], static_cast<double>(x.x), q4[1] * static_cast<double>(x.y)) +
+                              fma(q4[2], static_cast<double>(x.z), q4[3] * static_cast<double>(x.w));
+                    load(half + i, j0 + half + i + R * kWarps, bt);  // the next rows arrive during the sums
+                }
+                // butterfly: two steps hand each lane the sum of one row over 8 lanes, three more the whole sum
+#pragma unroll
+                for (int off = 16, n = 2; n >= 1; off >>= 1, n >>= 1) {
                     const bool up = (lane & off) != 0;
 #pragma unroll
                     for (int i = 0; i < n; ++i) {
@@ -112,16 +119,14 @@ __global__ void __launch_bounds__(kTopThreads) cache_select_kernel(const int32_t
                         part[i] = mine + __shfl_xor_sync(0xffffffffu, send, off);
                     }
                 }
-                part[0] += __shfl_xor_sync(0xffffffffu, part[0], 2);
-                part[0] += __shfl_xor_sync(0xffffffffu, part[0], 1);
-                const int r = ((lane >> 4) & 1) * 4 + ((lane >> 3) & 1) * 2 + ((lane >> 2) & 1);
-                if ((lane & 3) == 0 && j0 + r < bt) select_key[j0 + r] = score_key(static_cast<float>(part[0]));
+#pragma unroll
+                for (int off = 4; off > 0; off >>= 1) part[0] += __shfl_xor_sync(0xffffffffu, part[0], off);
+                const int j = j0 + half + (lane >> 3);  // lane bit 4: row bit 1, lane bit 3: row bit 0
+                if ((lane & 7) == 0 && j < bt) select_key[j] = score_key(static_cast<float>(part[0]));
             }
-            __syncthreads();
-            top_ascending(select_key, bt, want, out, sc);
         }
-    } else {
-        for (int i = tid; i < want; i += kTopThreads) out[i] = i;
+        __syncthreads();
+        top_blocks(select_key, bt, want, out, sc);
     }
     for (int i = want + tid; i < k; i += kTopThreads) out[i] = i == want ? bt : -1;
 }
@@ -372,6 +377,18 @@ __global__ void __launch_bounds__(128, CacheAttend<NH>::kPerSm) cache_attend_ker
         ++products_s;
     };
 
+    // rows of the next group's queries, asked for one tile ahead (up to 16 heads: registers)
+    constexpr int kQRows = NH <= 16 ? NH / 4 : 1;
+    uint2 q_next[kQRows];
+    auto load_q = [&](int bh) {
+#pragma unroll
+        for (int i = 0; i < kQRows; ++i)
+            if (warp + 4 * i < G)
+                q_next[i] = __ldg(reinterpret_cast<const uint2 *>(
+                                      q + (static_cast<size_t>(bh) * G + warp + 4 * i) * kCacheD) + lane);
+    };
+    if (NH <= 16) load_q(cur.b * Hk + cur.hk);
+
     float o[NH];
     int pair = -1;
     for (int it = 0; it < n_tiles; ++it) {
@@ -386,24 +403,29 @@ __global__ void __launch_bounds__(128, CacheAttend<NH>::kPerSm) cache_attend_ker
         }
         if (bh != pair) {  // a new group of query heads: two terms per element, two rows per head
             pair = bh;
-            for (int h = warp; h < G; h += 4) {
-                const uint2 w = __ldg(reinterpret_cast<const uint2 *>(q + (static_cast<size_t>(bh) * G + h) * kCacheD) + lane);
+#pragma unroll
+            for (int i = 0; i < NH / 4; ++i) {
+                const int h = warp + 4 * i;
+                if (h >= G) break;
+                const uint2 w = NH <= 16 ? q_next[i < kQRows ? i : 0]
+                                         : __ldg(reinterpret_cast<const uint2 *>(
+                                                     q + (static_cast<size_t>(bh) * G + h) * kCacheD) + lane);
                 const float x[4] = {__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u),
                                     __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u)};
                 uint32_t top = 0;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+                for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(x[e]) & 0x7FFFFFFFu);
                 top = __reduce_max_sync(0xffffffffu, top);
                 const bool finite = top < 0x7F800000u;
                 const float unit = finite ? e4m3_scale(__uint_as_float(top)) : 1.f, inv = pow2_inverse(unit);
                 uint32_t t0 = 0, t1 = 0;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float a = x[2 * i] * inv, c = x[2 * i + 1] * inv;
+                for (int e = 0; e < 2; ++e) {
+                    const float a = x[2 * e] * inv, c = x[2 * e + 1] * inv;
                     const uint16_t hi = pack_e4m3x2(a, c);
                     const float2 f = unpack_e4m3x2(hi);
-                    t0 |= static_cast<uint32_t>(hi) << (16 * i);
-                    t1 |= static_cast<uint32_t>(pack_e4m3x2((a - f.x) * 16.f, (c - f.y) * 16.f)) << (16 * i);
+                    t0 |= static_cast<uint32_t>(hi) << (16 * e);
+                    t1 |= static_cast<uint32_t>(pack_e4m3x2((a - f.x) * 16.f, (c - f.y) * 16.f)) << (16 * e);
                 }
                 const int unit16 = lane >> 2, in16 = (lane & 3) * 4, h1 = NH + h;
                 *reinterpret_cast<uint32_t *>(smem + SM::kQ + h * 128 + ((unit16 ^ (h & 7)) << 4) + in16) = t0;
@@ -420,6 +442,7 @@ __global__ void __launch_bounds__(128, CacheAttend<NH>::kPerSm) cache_attend_ker
             fence_proxy_async_smem();
             __syncthreads();
         }
+        if (NH <= 16 && last && it + 1 < n_tiles) load_q(pos1.b * Hk + pos1.hk);
         bool ok = true;
         if (tid == 0 && products_s == it) {
             ok = mbar_wait(bar_k, ph, abort_flag, 0x711);
@@ -637,8 +660,8 @@ __global__ void __launch_bounds__(128, CacheAttend<NH>::kPerSm) cache_attend_ker
 
 // ---------------------------------------------------------------------------
 // Joining the partials: M = max m_i, l = sum 2^(m_i - M) l_i, o = sum 2^(m_i - M) o_i / l, in the order of the
-// CTAs.  grid (B * Hk, head CTAs + weight CTAs): a head CTA joins 8 / WPH query heads, WPH warps each; a weight
-// CTA adds up the attention weight of 256 blocks over the group's heads.  WPH = 8 where a pair is split over
+// CTAs.  The first head_ctas CTAs join 8 / WPH query heads each, WPH warps per head; every CTA after them adds
+// up the attention weight of 256 blocks of one pair over its group's heads.  WPH = 8 where a pair is split over
 // many CTAs (few sequences), 1 where there are many pairs of few partials.
 // ---------------------------------------------------------------------------
 struct CachePartials {
@@ -679,24 +702,28 @@ __global__ void __launch_bounds__(256) cache_combine_kernel(const int32_t *__res
                                                             const float2 *block_ml, const int32_t *idx,
                                                             __nv_bfloat16 *__restrict__ o, float *__restrict__ lse,
                                                             const float *weight_in, float *weight_out, int B, int Hk,
-                                                            int G, int T, int s, int k, int nb, int grid) {
-    constexpr int kHeads = 8 / WPH;  // per head CTA
+                                                            int G, int T, int s, int k, int nb, int grid,
+                                                            int head_ctas) {
     __shared__ float2 head[kCacheMaxGroup];
     __shared__ float4 part[8][32];
-    const int bh = blockIdx.x, b = bh / Hk, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const bool heads = static_cast<int>(blockIdx.x) < head_ctas;
+    const int chunks = (nb + 255) / 256, w = blockIdx.x - head_ctas;
+    const int row = (blockIdx.x * 8 + warp) / WPH;  // query head of the batch (head CTAs)
+    const int bh = heads ? min(row / G, B * Hk - 1) : w / chunks, b = bh / Hk;
     const int L = __ldg(cache_len + b), nt = cache_tiles(L, T, s, k), ns = cache_slots(L, T, s, k);
     const int64_t total = cache_total_tiles(cache_len, B, Hk, T, s, k, lane);
     const int64_t first = cache_tiles_before(cache_len, b, T, s, k, lane) * Hk + static_cast<int64_t>(bh % Hk) * nt;
-    const int head_ctas = (G + kHeads - 1) / kHeads;
-    grid_dependency_wait();
     CachePartials P{0, 0};
     if (nt > 0) P = cache_partials_of(total, first, nt, grid, bh);
     const float2 *ml = mlpart + P.slot0 * G;
-    if (static_cast<int>(blockIdx.y) < head_ctas) {
-        const int h = blockIdx.y * kHeads + warp / WPH, grp = warp % WPH;
+    grid_dependency_wait();
+    if (heads) {
+        const int h = row % G, grp = warp % WPH;
+        const bool mine = row < B * Hk * G;
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
         float2 t = make_float2(-INFINITY, 0.f);
-        if (h < G && nt > 0) {
+        if (mine && nt > 0) {
             t = cache_join(ml, P.n, G, h, lane);
             const float4 *op = reinterpret_cast<const float4 *>(opart + (P.slot0 * G + h) * kCacheD) + lane;
 #pragma unroll 8
@@ -716,39 +743,39 @@ __global__ void __launch_bounds__(256) cache_combine_kernel(const int32_t *__res
                     a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
                 }
         }
-        if (h < G && grp == 0) {
+        if (mine && grp == 0) {
             const float inv = nt > 0 ? 1.f / t.y : 0.f;  // no token (or a bad length): o = 0
-            const size_t row = static_cast<size_t>(bh) * G + h;
-            reinterpret_cast<uint2 *>(o + row * kCacheD)[lane] =
+            reinterpret_cast<uint2 *>(o + static_cast<size_t>(row) * kCacheD)[lane] =
                 make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
             if (lane == 0) lse[row] = nt > 0 ? fmaf(t.x, kLn2, logf(t.y)) : -INFINITY;
         }
         return;
     }
     // attention weight of blocks [j0, j0 + 256)
-    const int j0 = (blockIdx.y - head_ctas) * 256, j = j0 + tid;
+    const int j0 = w % chunks * 256, j = j0 + tid;
+    const size_t at = static_cast<size_t>(bh) * nb + j;
+    const float before = weight_in && j < nb ? weight_in[at] : 0.f;
     if (nt > 0) {
         for (int h = warp; h < G; h += 8) {
             const float2 t = cache_join(ml, P.n, G, h, lane);
             if (lane == 0) head[h] = t;
         }
-        __syncthreads();
     }
     auto mass = [&](int slot, int slots) {  // of one attended block
-        float w = 0.f;
+        float sum = 0.f;
         const float2 *bl = block_ml + static_cast<size_t>(bh) * G * slots + slot;
 #pragma unroll 4
         for (int h = 0; h < G; ++h) {
             const float2 a = __ldcg(bl + static_cast<size_t>(h) * slots);
-            w += a.y * fast_exp2(a.x - head[h].x) / head[h].y;
+            sum += a.y * fast_exp2(a.x - head[h].x) / head[h].y;
         }
-        return w;
+        return sum;
     };
-    const size_t at = static_cast<size_t>(bh) * nb + j;
     if (k == 0) {
-        if (j < nb) weight_out[at] = (weight_in ? weight_in[at] : 0.f) + (j < ns ? mass(j, nb) : 0.f);
+        __syncthreads();
+        if (j < nb) weight_out[at] = before + (j < ns ? mass(j, nb) : 0.f);
     } else {
-        if (j < nb) weight_out[at] = weight_in ? weight_in[at] : 0.f;
+        if (j < nb) weight_out[at] = before;
         __syncthreads();
         for (int i = tid; i < ns; i += 256) {  // attended blocks are distinct
             const int jj = __ldcg(idx + static_cast<size_t>(bh) * k + i);

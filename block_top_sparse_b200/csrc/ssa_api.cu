@@ -1013,10 +1013,12 @@ ssa_status_t ssa_cache_decode(const ssa_dims_t *dims, const int32_t *cache_len, 
     // partials per pair: about grid / pairs, each of 128 values per head
     const unsigned grid = cache_grid(S.G);
     const bool wide = grid / bhk >= 16;
-    const unsigned head_ctas = wide ? S.G : (S.G + 7) / 8, weight_ctas = weight_out ? (S.nb + 255) / 256 : 0;
-    if (!launch_dependent(wide ? cache_combine_kernel<8> : cache_combine_kernel<1>, dim3(bhk, head_ctas + weight_ctas), 256,
-                          0, st, cache_len, opart, ml, block_ml, idx, static_cast<__nv_bfloat16 *>(o), lse, weight_in,
-                          weight_out, S.B, S.Hk, S.G, S.T, S.s, S.k, S.nb, static_cast<int>(grid)))
+    const unsigned rows = static_cast<unsigned>(S.BH), head_ctas = wide ? rows : (rows + 7) / 8;
+    const size_t weight_ctas = weight_out ? S.BHk * ((S.nb + 255) / 256) : 0;
+    if (!launch_dependent(wide ? cache_combine_kernel<8> : cache_combine_kernel<1>,
+                          dim3(static_cast<unsigned>(head_ctas + weight_ctas)), 256, 0, st, cache_len, opart, ml, block_ml,
+                          idx, static_cast<__nv_bfloat16 *>(o), lse, weight_in, weight_out, S.B, S.Hk, S.G, S.T, S.s, S.k,
+                          S.nb, static_cast<int>(grid), static_cast<int>(head_ctas)))
         return SSA_ERR_CUDA;
     return launch_status();
 }

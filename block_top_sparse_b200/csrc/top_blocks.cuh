@@ -7,7 +7,8 @@
 // far, give the kk-th largest key; the chosen indices are those above it and
 // the first ones equal to it, written in ascending order from ballots.  The
 // counts do not depend on the order of the additions, so neither does the
-// result; the cost is 4n / 256 steps of the CTA, whatever kk.
+// result; the cost is 4n / 256 steps of the CTA, whatever kk.  Below 1024 keys one
+// warp searches them in its registers instead.
 #pragma once
 
 #include "device.cuh"
@@ -106,6 +107,79 @@ __device__ __forceinline__ void top_ascending(const uint32_t *keys, int n, int k
         if (gt || (eq && eq_at + eq_before < left)) out[rank] = i;
         at += gt_all + min(eq_at + eq_all, left) - min(eq_at, left);
         eq_at += eq_all;
+    }
+}
+
+// The same for n < 1024 by one warp, the keys in its registers (KPL per lane, n <= 32 * KPL): the kk-th
+// largest key is found two bits at a time from the first bit in which the keys differ (three candidates'
+// counts, 11 bits each, in one warp sum), stopping early at a candidate with exactly kk keys at or above it.
+// No barrier; a third of the time of the CTA's counts for 256 keys.
+template <int KPL>
+__device__ __forceinline__ void top_ascending_warp(const uint32_t *keys, int n, int kk, int32_t *out, int lane) {
+    uint32_t key[KPL], hi = 0u, lo = 0xFFFFFFFFu;
+#pragma unroll
+    for (int i = 0; i < KPL; ++i) {
+        const int j = 32 * i + lane;
+        key[i] = j < n ? keys[j] : 0u;  // never at or above a candidate
+        if (j < n) hi = max(hi, key[i]), lo = min(lo, key[i]);
+    }
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    uint32_t tau = hi;
+    bool exact = false;
+    if (hi != lo) {
+        int b = (31 - __clz(hi ^ lo)) | 1;
+        tau = b == 31 ? 0u : hi & (0xFFFFFFFFu << (b + 1));  // at least kk keys are >= tau throughout
+#pragma unroll 1
+        for (; b > 0 && !exact; b -= 2) {
+            const uint32_t c1 = tau + (1u << (b - 1)), c2 = tau + (2u << (b - 1)), c3 = tau + (3u << (b - 1));
+            uint32_t cnt = 0;
+#pragma unroll
+            for (int i = 0; i < KPL; ++i)
+                cnt += (key[i] >= c1 ? 1u : 0u) + (key[i] >= c2 ? 1u << 11 : 0u) + (key[i] >= c3 ? 1u << 22 : 0u);
+            cnt = __reduce_add_sync(0xffffffffu, cnt);
+            const int n1 = cnt & 2047, n2 = (cnt >> 11) & 2047, n3 = cnt >> 22;
+            int m = n;
+            if (n3 >= kk)
+                tau = c3, m = n3;
+            else if (n2 >= kk)
+                tau = c2, m = n2;
+            else if (n1 >= kk)
+                tau = c1, m = n1;
+            exact = m == kk;
+        }
+    }
+    int left = 0;  // of the keys equal to tau, lowest index first
+    if (!exact) {
+        unsigned gt = 0;
+#pragma unroll
+        for (int i = 0; i < KPL; ++i) gt += key[i] > tau ? 1u : 0u;
+        left = kk - static_cast<int>(__reduce_add_sync(0xffffffffu, gt));
+    }
+    const unsigned below = (1u << lane) - 1u;
+    int at = 0, eq_at = 0;
+#pragma unroll
+    for (int i = 0; i < KPL; ++i) {
+        if (32 * i >= n) break;
+        const bool in = 32 * i + lane < n, eq = !exact && in && key[i] == tau;
+        const unsigned be = __ballot_sync(0xffffffffu, eq);
+        const bool chosen = in && (exact ? key[i] >= tau : key[i] > tau || (eq && eq_at + __popc(be & below) < left));
+        const unsigned bc = __ballot_sync(0xffffffffu, chosen);
+        if (chosen) out[at + __popc(bc & below)] = 32 * i + lane;
+        at += __popc(bc);
+        eq_at += __popc(be);
+    }
+}
+
+// Either of the two, by the number of keys (uniform over the CTA).
+__device__ __forceinline__ void top_blocks(const uint32_t *keys, int n, int kk, int32_t *out, TopScratch &sc) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (n <= 256) {
+        if (warp == 0) top_ascending_warp<8>(keys, n, kk, out, lane);
+    } else if (n < 1024) {
+        if (warp == 0) top_ascending_warp<32>(keys, n, kk, out, lane);
+    } else {
+        top_ascending(keys, n, kk, out, sc);
     }
 }
 
