@@ -120,10 +120,18 @@ def _p(t) -> Optional[int]:
     return t.data_ptr()
 
 
+_raw_stream = None
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
+        global _raw_stream
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        if _raw_stream is None:
+            # the handle without a Stream object around it (3 us less per call), where this torch has it
+            _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+                lambda device: torch.cuda.current_stream(device).cuda_stream)
+        return _raw_stream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -219,14 +227,18 @@ def ssa_rope(dims, X, heads, pos0=0, base=10000.0, factor=1.0, transpose=0, stre
                                        _stream(stream)))
 
 
+_Int64x3 = ctypes.c_int64 * 3
+
+
 def _strides(t):
     """Element strides (batch, head, token) of a [B, heads, T, d] tensor as the host array that the library reads;
     None for a contiguous one, a missing one or an address."""
     if t is None or isinstance(t, int) or t.is_contiguous():
         return None
-    if t.stride(3) != 1:
-        raise ValueError("the elements of a row must be adjacent (stride %d)" % t.stride(3))
-    return (ctypes.c_int64 * 3)(*t.stride()[:3])
+    b, h, r, e = t.stride()
+    if e != 1:
+        raise ValueError("the elements of a row must be adjacent (stride %d)" % e)
+    return _Int64x3(b, h, r)
 
 
 def ssa_rope_axes(dims, pos, sections, Q, Qr, K=None, Kr=None, flags=0, base=10000.0, factor=1.0, stream=None):

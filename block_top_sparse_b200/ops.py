@@ -103,20 +103,20 @@ def rope(dims: L.Dims, X: torch.Tensor, pos0: int = 0, base: float = 10000.0, fa
     return X
 
 
-def _is(t: torch.Tensor, name: str, shape, dtype, device, strided: bool = False) -> None:
-    """ValueError unless t is what the call reads: the library sees its address only."""
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device:
-        raise ValueError("%s must be %s %s on %s, got %s %s on %s" % (name, list(shape), dtype, device, list(t.shape),
-                                                                      t.dtype, t.device))
-    if not strided and not t.is_contiguous():
+def _is(t: torch.Tensor, name: str, shape: tuple, dtype, device: int, strided: bool = False) -> None:
+    """ValueError unless t is what the call reads (the library sees its address only); device: a CUDA device's index."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != device:
+        raise ValueError("%s must be %s %s on cuda:%d, got %s %s on %s" % (name, list(shape), dtype, device,
+                                                                           list(t.shape), t.dtype, t.device))
+    if not (strided or t.is_contiguous()):
         raise ValueError("%s must be contiguous" % name)
 
 
-def _device_of(t: torch.Tensor) -> torch.device:
-    """The device that a call runs on: its tensors' device, which must be the current one."""
-    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+def _device_of(t: torch.Tensor) -> int:
+    """Index of the device that a call runs on: its tensors' device, which must be the current one."""
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
         raise ValueError("tensors must be on the current CUDA device, got %s" % t.device)
-    return t.device
+    return t.get_device()
 
 
 def rope_axes(dims: L.Dims, pos: torch.Tensor, sections, Q: torch.Tensor, K: Optional[torch.Tensor] = None,
@@ -136,8 +136,7 @@ def rope_axes(dims: L.Dims, pos: torch.Tensor, sections, Q: torch.Tensor, K: Opt
     if K is not None:
         _is(K, "K", kshape, dtype, dev, True)
     if out is None:
-        Qr = torch.empty(shape, dtype=dtype, device=dev)
-        Kr = None if K is None else torch.empty(kshape, dtype=dtype, device=dev)
+        Qr, Kr = Q.new_empty(shape), None if K is None else K.new_empty(kshape)
     else:
         Qr, Kr = out
         _is(Qr, "out[0]", shape, dtype, dev, True)
@@ -171,13 +170,18 @@ class Cache8(NamedTuple):
         return Cache8(codes(), scale(), codes(), scale(),
                       torch.empty((B, Hk, nb, dims.d), dtype=torch.float32, device=device) if pooled else None)
 
-    def check(self, dims: L.Dims, device) -> None:
-        B, Hk, nb = dims.B, dims.kv_heads, dims.T // dims.s
-        for name, codes, scale in (("K", self.K8, self.Kscale), ("V", self.V8, self.Vscale)):
-            _is(codes, name + "8", (B, Hk, dims.T, dims.d), torch.float8_e4m3fn, device)
-            _is(scale, name + "scale", (B, Hk, nb), torch.float32, device)
-        if self.Kbar is not None:
-            _is(self.Kbar, "Kbar", (B, Hk, nb, dims.d), torch.float32, device)
+    def check(self, dims: L.Dims, device: int) -> tuple:
+        """ValueError unless the buffers are those of dims; returns the shape of the scales."""
+        K8, Kscale, V8, Vscale, Kbar = self
+        B, Hk, T, d = dims.B, dims.Hkv or dims.H, dims.T, dims.d
+        codes, scales = (B, Hk, T, d), (B, Hk, T // dims.s)
+        _is(K8, "K8", codes, torch.float8_e4m3fn, device)
+        _is(V8, "V8", codes, torch.float8_e4m3fn, device)
+        _is(Kscale, "Kscale", scales, torch.float32, device)
+        _is(Vscale, "Vscale", scales, torch.float32, device)
+        if Kbar is not None:
+            _is(Kbar, "Kbar", scales + (d,), torch.float32, device)
+        return scales
 
 
 def cache_append(dims: L.Dims, cache: Cache8, cache_len: torch.Tensor, K: torch.Tensor, V: torch.Tensor,
@@ -205,15 +209,16 @@ def cache_decode(dims: L.Dims, cache: Cache8, cache_len: torch.Tensor, q: torch.
     dev = _device_of(q)
     _is(q, "q", (dims.B, dims.H, dims.d), torch.bfloat16, dev)
     _is(cache_len, "cache_len", (dims.B,), torch.int32, dev)
-    cache.check(dims, dev)
-    for name, w in (("weight_in", weight_in), ("weight_out", weight_out)):
-        if w is not None:
-            _is(w, name, (dims.B, dims.kv_heads, dims.T // dims.s), torch.float32, dev)
+    scales = cache.check(dims, dev)
+    if weight_in is not None:
+        _is(weight_in, "weight_in", scales, torch.float32, dev)
+    if weight_out is not None:
+        _is(weight_out, "weight_out", scales, torch.float32, dev)
     o = torch.empty_like(q)
-    lse = torch.empty((dims.B, dims.H), dtype=torch.float32, device=dev)
-    idx = torch.empty((dims.B, dims.kv_heads, dims.k), dtype=torch.int32, device=dev) if dims.k > 0 else None
+    lse = cache.Kscale.new_empty((dims.B, dims.H))
+    idx = cache_len.new_empty((dims.B, dims.kv_heads, dims.k)) if dims.k > 0 else None
     if ws is None:
-        ws = _ws(dims, L.SSA_OP_CACHE_DECODE, dev)
+        ws = _ws(dims, L.SSA_OP_CACHE_DECODE, q.device)
     L.ssa_cache_decode(dims, cache_len, q, cache.K8, cache.Kscale, cache.V8, cache.Vscale, cache.Kbar, idx, o, lse,
                        weight_in, weight_out, ws)
     return o, lse, idx
@@ -226,18 +231,18 @@ def cache_evict(dims: L.Dims, cache: Cache8, cache_len: torch.Tensor, keep: int,
     ones of greatest weight [B, Hkv, T/s]; the cache is compacted in place.  weight_out (may be weight) receives the
     weights in the new order, new_len (default: a new tensor; may be cache_len) the lengths.  Returns (kept, new_len)."""
     dev = _device_of(weight)
-    _is(weight, "weight", (dims.B, dims.kv_heads, dims.T // dims.s), torch.float32, dev)
     _is(cache_len, "cache_len", (dims.B,), torch.int32, dev)
-    cache.check(dims, dev)
+    scales = cache.check(dims, dev)
+    _is(weight, "weight", scales, torch.float32, dev)
     if weight_out is not None:
-        _is(weight_out, "weight_out", weight.shape, torch.float32, dev)
+        _is(weight_out, "weight_out", scales, torch.float32, dev)
     if new_len is None:
         new_len = torch.empty_like(cache_len)
     else:
         _is(new_len, "new_len", (dims.B,), torch.int32, dev)
-    kept = torch.empty((dims.B, dims.kv_heads, max(int(keep), 0)), dtype=torch.int32, device=dev)
+    kept = cache_len.new_empty((dims.B, dims.kv_heads, max(int(keep), 0)))
     if ws is None:
-        ws = _ws(dims, L.SSA_OP_CACHE_EVICT, dev)
+        ws = _ws(dims, L.SSA_OP_CACHE_EVICT, weight.device)
     L.ssa_cache_evict(dims, keep, cache_len, weight, cache.K8, cache.Kscale, cache.V8, cache.Vscale, kept, cache.Kbar,
                       weight_out, new_len, sink, recent, ws)
     return kept, new_len
