@@ -13,17 +13,17 @@
 // error of the order of fp32's own rounding at any 32-bit position.
 //
 // One CTA per `rows` consecutive tokens (flattened over the sequences) and
-// slice of heads: the tokens' cosines and sines are computed once and shared by
-// the slice's heads; each thread turns 16-byte pieces of a row's two halves,
-// four rows' loads in flight.  HBM-bound: one read and one write of the
-// tensors.
+// slice of heads: the tokens' cosines and sines are computed once.  A thread
+// keeps those of one token's 16-byte piece in registers and walks down the
+// heads with them, four heads' loads (both halves of the row) in flight.
+// HBM-bound: one read and one write of the tensors.
 #pragma once
 
 #include "device.cuh"
 
 namespace ssa {
 
-constexpr int kRopeAxesRows = 16;     // most tokens per CTA
+constexpr int kRopeAxesRows = 16;     // most tokens per CTA (a power of two)
 constexpr int kRopeAxesThreads = 256;
 constexpr int kRopeMaxAxes = 4;
 
@@ -40,9 +40,9 @@ struct RopeAxesTensor {
     int heads;  // 0: no such tensor
 };
 
+// Elements of a 16-byte piece.
 template <typename T>
-__device__ __forceinline__ void rope_load(const T *x, float (&v)[16 / sizeof(T)]) {
-    const uint4 w = *reinterpret_cast<const uint4 *>(x);
+__device__ __forceinline__ void rope_unpack(const uint4 &w, float (&v)[16 / sizeof(T)]) {
     const uint32_t p[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -56,7 +56,7 @@ __device__ __forceinline__ void rope_load(const T *x, float (&v)[16 / sizeof(T)]
 }
 
 template <typename T>
-__device__ __forceinline__ void rope_store(T *x, const float (&v)[16 / sizeof(T)]) {
+__device__ __forceinline__ uint4 rope_pack(const float (&v)[16 / sizeof(T)]) {
     uint32_t p[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -65,60 +65,50 @@ __device__ __forceinline__ void rope_store(T *x, const float (&v)[16 / sizeof(T)
         else
             p[q] = __float_as_uint(v[q]);
     }
-    *reinterpret_cast<uint4 *>(x) = make_uint4(p[0], p[1], p[2], p[3]);
+    return make_uint4(p[0], p[1], p[2], p[3]);
 }
 
-// Rows [head h0 .. h1) x [the CTA's nt tokens] of one tensor.  `in` may be `out`: a thread reads both
-// pieces of a row before it writes them, and no other thread touches them.
+// One token's piece of heads h, h + step, .. below h1 of one tensor, from `in` to `out` (this piece of head 0).
+// They may be the same: a thread reads both halves of a row before it writes them, and no other thread
+// touches them.
 template <typename T>
-__device__ __forceinline__ void rope_axes_rows(const RopeAxesTensor &X, const float2 (*cs)[64], const int64_t *in_at,
-                                               const int64_t *out_at, int h0, int h1, int nt, int half) {
+__device__ __forceinline__ void rope_axes_heads(const RopeAxesTensor &X, const T *in, T *out, int h, int h1, int step,
+                                                int half, const float2 (&cs)[16 / sizeof(T)]) {
     constexpr int V = 16 / sizeof(T), U = 4;
-    const int units = half / V, rpp = kRopeAxesThreads / units;
-    const int u = threadIdx.x % units, rr = threadIdx.x / units;
-    const int rows = (h1 - h0) * nt;
-    for (int row0 = rr; row0 < rows; row0 += U * rpp) {
-        float a[U][V], c[U][V];
-        int64_t to[U];
-        int tok[U];
+    for (; h < h1; h += U * step) {
+        uint4 a[U], c[U];
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-            const int row = row0 + i * rpp;
-            if (row < rows) {
-                const int h = h0 + row / nt;
-                tok[i] = row % nt;
-                const T *x = static_cast<const T *>(X.in) + in_at[tok[i]] + h * X.is[1] + u * V;
-                to[i] = out_at[tok[i]] + h * X.os[1] + u * V;
-                rope_load<T>(x, a[i]);
-                rope_load<T>(x + half, c[i]);
+        for (int i = 0; i < U; ++i)
+            if (h + i * step < h1) {
+                const T *x = in + (h + i * step) * X.is[1];
+                a[i] = *reinterpret_cast<const uint4 *>(x);
+                c[i] = *reinterpret_cast<const uint4 *>(x + half);
             }
-        }
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-            if (row0 + i * rpp < rows) {
-                float y0[V], y1[V];
+        for (int i = 0; i < U; ++i)
+            if (h + i * step < h1) {
+                float x0[V], x1[V], y0[V], y1[V];
+                rope_unpack<T>(a[i], x0);
+                rope_unpack<T>(c[i], x1);
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    const float2 t = cs[tok[i]][u * V + v];
-                    y0[v] = a[i][v] * t.x - c[i][v] * t.y;
-                    y1[v] = a[i][v] * t.y + c[i][v] * t.x;
+                    y0[v] = x0[v] * cs[v].x - x1[v] * cs[v].y;
+                    y1[v] = x0[v] * cs[v].y + x1[v] * cs[v].x;
                 }
-                T *y = static_cast<T *>(X.out) + to[i];
-                rope_store<T>(y, y0);
-                rope_store<T>(y + half, y1);
+                T *y = out + (h + i * step) * X.os[1];
+                *reinterpret_cast<uint4 *>(y) = rope_pack<T>(y0);
+                *reinterpret_cast<uint4 *>(y + half) = rope_pack<T>(y1);
             }
-        }
     }
 }
 
 // grid (ceil(B*T / rows), head slices); heads_per = query heads, then key heads, of one slice.
 template <typename T>
-__global__ void __launch_bounds__(kRopeAxesThreads) rope_axes_kernel(
+__global__ void __launch_bounds__(kRopeAxesThreads, 3) rope_axes_kernel(
     const __grid_constant__ RopeAxesTable tab, const int32_t *__restrict__ pos, int64_t BT, int T_len, int half,
     int rows, int heads_per, float sign, const __grid_constant__ RopeAxesTensor Q,
     const __grid_constant__ RopeAxesTensor K) {
     __shared__ float2 cs[kRopeAxesRows][64];
-    __shared__ int64_t at[4][kRopeAxesRows];  // element offsets of the tokens: Q in, Q out, K in, K out
     const int64_t f0 = static_cast<int64_t>(blockIdx.x) * rows;
     const int nt = static_cast<int>(min(static_cast<int64_t>(rows), BT - f0));
     for (int e = threadIdx.x; e < nt * half; e += kRopeAxesThreads) {
@@ -131,17 +121,25 @@ __global__ void __launch_bounds__(kRopeAxesThreads) rope_axes_kernel(
         sincospif(2.f * rf, &s, &c);
         cs[tt][i] = make_float2(fmaf(-e1, s, c), sign * fmaf(e1, c, s));
     }
-    if (threadIdx.x < nt) {
-        const int64_t f = f0 + threadIdx.x, b = f / T_len, t = f % T_len;
-        at[0][threadIdx.x] = b * Q.is[0] + t * Q.is[2];
-        at[1][threadIdx.x] = b * Q.os[0] + t * Q.os[2];
-        at[2][threadIdx.x] = b * K.is[0] + t * K.is[2];
-        at[3][threadIdx.x] = b * K.os[0] + t * K.os[2];
-    }
     __syncthreads();
+    // thread: 16-byte piece u of token tt, heads hg, hg + step, .. (rows * units divides the CTA)
+    constexpr int V = 16 / sizeof(T);
+    const int units = half / V, u = threadIdx.x % units, tt = threadIdx.x / units % rows;
+    const int hg = threadIdx.x / units / rows, step = kRopeAxesThreads / units / rows;
+    if (tt >= nt) return;
+    float2 mine[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) mine[v] = cs[tt][u * V + v];
+    const int64_t f = f0 + tt, b = f / T_len, t = f % T_len;
     const int h0 = blockIdx.y * heads_per, h1 = min(h0 + heads_per, Q.heads + K.heads);
-    if (h0 < Q.heads) rope_axes_rows<T>(Q, cs, at[0], at[1], h0, min(h1, Q.heads), nt, half);
-    if (h1 > Q.heads) rope_axes_rows<T>(K, cs, at[2], at[3], max(h0 - Q.heads, 0), h1 - Q.heads, nt, half);
+    if (h0 < Q.heads)
+        rope_axes_heads<T>(Q, static_cast<const T *>(Q.in) + b * Q.is[0] + t * Q.is[2] + u * V,
+                           static_cast<T *>(Q.out) + b * Q.os[0] + t * Q.os[2] + u * V, h0 + hg, min(h1, Q.heads), step,
+                           half, mine);
+    if (h1 > Q.heads)
+        rope_axes_heads<T>(K, static_cast<const T *>(K.in) + b * K.is[0] + t * K.is[2] + u * V,
+                           static_cast<T *>(K.out) + b * K.os[0] + t * K.os[2] + u * V, max(h0 - Q.heads, 0) + hg,
+                           h1 - Q.heads, step, half, mine);
 }
 
 }  // namespace ssa

@@ -911,11 +911,11 @@ ssa_status_t ssa_rope_axes(const ssa_dims_t *dims, const int32_t *pos, int axes,
         if (flags & SSA_ROPE_INTERLEAVED) a = (a + 1) % axes;
     }
     for (int i = half; i < 64; ++i) tab.axis[i] = 0, tab.turns[i] = 0.0;
-    // tokens per CTA: 16 where there are many (the angles are shared by the heads), down to one, so that two
-    // CTAs' worth per SM share the work; then the heads are split while SMs are still idle
+    // tokens per CTA: 16 where there are many (the angles are shared by the heads), down to one, so that at
+    // least two CTAs per SM share the work; then the heads are split while SMs are still idle
     const int heads = XQ.heads + XK.heads;
-    const int64_t want = (BT + 2 * kCacheSms - 1) / (2 * kCacheSms);
-    const int rows = static_cast<int>(want < 1 ? 1 : want > kRopeAxesRows ? kRopeAxesRows : want);
+    int rows = 1;
+    while (rows < kRopeAxesRows && BT > static_cast<int64_t>(rows) * 2 * kCacheSms) rows *= 2;
     const int64_t ctas = (BT + rows - 1) / rows;
     int slices = static_cast<int>(2 * kCacheSms / ctas);
     slices = slices < 1 ? 1 : slices > (heads + 7) / 8 ? (heads + 7) / 8 : slices;
