@@ -57,15 +57,15 @@ struct CacheRows {
     int64_t st[3];
 };
 
-// grid (B * Hk, blocks that n rows can touch, 2: keys, values), 256 threads: 16 threads of 8 elements per
-// row, 16 rows per pass.
+// grid (B * Hk, blocks that n rows can touch, 2: keys, values), 2 S threads: 16 threads of 8 elements per row,
+// eight passes over the block's rows, all of them in flight at once.
 template <int S>
-__global__ void __launch_bounds__(256) cache_append_kernel(
+__global__ void __launch_bounds__(2 * S) cache_append_kernel(
     const int32_t *__restrict__ cache_len, const int32_t *__restrict__ n_new, int n, const CacheRows K,
     const CacheRows V, uint8_t *K8, float *Kscale, uint8_t *V8, float *Vscale, float *Kbar, int Hk, int T) {
-    constexpr int P = S / 16;
-    __shared__ uint32_t red[8];
-    __shared__ float col[16][kCacheD];
+    constexpr int P = 8, kRows = S / P, kWarps = S / 16;  // rows per pass
+    __shared__ uint32_t red[kWarps];
+    __shared__ float col[kRows][kCacheD];
     const int bh = blockIdx.x, b = bh / Hk, hk = bh % Hk;
     const int L = __ldg(cache_len + b), nn = n_new ? __ldg(n_new + b) : n;
     if (L < 0 || nn < 0 || nn > n || nn > T - L) {  // nothing is written for this sequence
@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(256) cache_append_kernel(
     uint32_t top2 = 0;  // largest magnitude bits, even and odd elements
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-        const int r = rr + 16 * p;
+        const int r = rr + kRows * p;
         v[p] = make_uint4(0u, 0u, 0u, 0u);
         if (r >= r0 && r < r1) v[p] = __ldg(reinterpret_cast<const uint4 *>(x + r * X.st[2]));
     }
@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(256) cache_append_kernel(
         __syncthreads();
         m = red[0];
 #pragma unroll
-        for (int w = 1; w < 8; ++w) m = max(m, red[w]);
+        for (int w = 1; w < kWarps; ++w) m = max(m, red[w]);
         return m;
     };
     uint32_t top = block_max(max(top2 & 0xFFFFu, top2 >> 16));
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(256) cache_append_kernel(
     };
     if (r0 > 0 && (want > old || pool)) {  // older rows: moved to a larger scale, or summed
         const float ratio = old * inv;
-        for (int r = rr; r < r0; r += 16) {
+        for (int r = rr; r < r0; r += kRows) {
             uint2 *q = reinterpret_cast<uint2 *>(codes + r * kCacheD + u * 8);
             uint2 w = *q;
             if (want > old) {
@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(256) cache_append_kernel(
     }
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-        const int r = rr + 16 * p;
+        const int r = rr + kRows * p;
         if (r < r0 || r >= r1) continue;
         const uint32_t w[4] = {v[p].x, v[p].y, v[p].z, v[p].w};
         uint32_t c[4];
@@ -183,8 +183,102 @@ __global__ void __launch_bounds__(256) cache_append_kernel(
         if (threadIdx.x < kCacheD) {
             float a = 0.f;
 #pragma unroll
-            for (int r = 0; r < 16; ++r) a += col[r][threadIdx.x];
+            for (int r = 0; r < kRows; ++r) a += col[r][threadIdx.x];
             Kbar[block * kCacheD + threadIdx.x] = a / static_cast<float>(S) * want;  // (both powers of two)
+        }
+    }
+}
+
+// One new token per sequence (n = 1): a warp per (sequence, key head), lanes 0-15 the key, lanes 16-31 the
+// value, no barrier; grid ceil(B * Hk / 4).  The decode step's form: its time is that of the loads after one
+// another (length, row and scale, store).
+template <int S>
+__global__ void __launch_bounds__(128) cache_append_token_kernel(
+    const int32_t *__restrict__ cache_len, const int32_t *__restrict__ n_new, const CacheRows K, const CacheRows V,
+    uint8_t *K8, float *Kscale, uint8_t *V8, float *Vscale, float *Kbar, int pairs, int Hk, int T) {
+    const int bh = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31, side = lane >> 4, u = lane & 15;
+    if (bh >= pairs) return;
+    const int b = bh / Hk, hk = bh % Hk;
+    const CacheRows &X = side ? V : K;
+    // the row does not depend on the length: both are asked for at once
+    const uint4 v = __ldg(reinterpret_cast<const uint4 *>(X.p + b * X.st[0] + hk * X.st[1] + u * 8));
+    const int L = __ldg(cache_len + b), nn = n_new ? __ldg(n_new + b) : 1;
+    if (L < 0 || nn < 0 || nn > 1 || nn > T - L) {
+        if (lane == 0) record_error(ERR_CACHE_INPUT, 0x704);
+        return;
+    }
+    if (nn == 0) return;
+    const int j = L / S, r0 = L % S;
+    const size_t block = static_cast<size_t>(bh) * (T / S) + j;
+    uint8_t *codes = (side ? V8 : K8) + block * S * kCacheD + u * 8;
+    float *scale = (side ? Vscale : Kscale) + block;
+    const float old = r0 > 0 ? *scale : 0.f;
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t top = 0, finite = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t lo = w[i] & 0x7FFFu, hi = (w[i] >> 16) & 0x7FFFu;
+        top = max(top, max(lo, hi));
+        if (lo < 0x7F80u) finite = max(finite, lo);
+        if (hi < 0x7F80u) finite = max(finite, hi);
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) {
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        finite = max(finite, __shfl_xor_sync(0xffffffffu, finite, o));
+    }
+    const float want = fmaxf(e4m3_scale(__uint_as_float(finite << 16)), old), inv = pow2_inverse(want);
+    if (r0 > 0 && want > old) {  // the older rows move to the larger scale
+        const float ratio = old * inv;
+#pragma unroll 8
+        for (int r = 0; r < r0; ++r) {
+            uint2 *q = reinterpret_cast<uint2 *>(codes + r * kCacheD);
+            uint32_t c[2] = {q->x, q->y};
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float2 a = unpack_e4m3x2(static_cast<uint16_t>(c[i]));
+                const float2 d = unpack_e4m3x2(static_cast<uint16_t>(c[i] >> 16));
+                c[i] = pack_e4m3x2(a.x * ratio, a.y * ratio) |
+                       static_cast<uint32_t>(pack_e4m3x2(d.x * ratio, d.y * ratio)) << 16;
+            }
+            *q = make_uint2(c[0], c[1]);
+        }
+    }
+    uint32_t c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float lo = __uint_as_float(w[i] << 16) * inv, hi = __uint_as_float(w[i] & 0xFFFF0000u) * inv;
+        if (top >= 0x7F80u) lo = (lo - lo) + lo, hi = (hi - hi) + hi;  // infinity -> NaN
+        c[i] = pack_e4m3x2(lo, hi);
+    }
+    *reinterpret_cast<uint2 *>(codes + r0 * kCacheD) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+    if (u == 0) *scale = want;
+    if (Kbar && r0 == S - 1) {  // the block is complete: the whole warp sums its keys, two rows at a time
+        __syncwarp();           // the rows just written
+        const float key_scale = __shfl_sync(0xffffffffu, want, 0);
+        const uint8_t *rows = K8 + block * S * kCacheD + side * kCacheD + u * 8;
+        float sum[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[i] = 0.f;
+#pragma unroll 16
+        for (int r = 0; r < S; r += 2) {
+            const uint2 q = *reinterpret_cast<const uint2 *>(rows + r * kCacheD);
+            const uint32_t p[2] = {q.x, q.y};
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float2 a = unpack_e4m3x2(static_cast<uint16_t>(p[i]));
+                const float2 d = unpack_e4m3x2(static_cast<uint16_t>(p[i] >> 16));
+                sum[4 * i] += a.x, sum[4 * i + 1] += a.y, sum[4 * i + 2] += d.x, sum[4 * i + 3] += d.y;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 16);
+        if (side == 0) {
+            float4 *to = reinterpret_cast<float4 *>(Kbar + block * kCacheD + u * 8);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                to[i] = make_float4(sum[4 * i] / S * key_scale, sum[4 * i + 1] / S * key_scale,
+                                    sum[4 * i + 2] / S * key_scale, sum[4 * i + 3] / S * key_scale);
         }
     }
 }

@@ -23,7 +23,7 @@
 
 namespace ssa {
 
-constexpr int kRopeAxesRows = 16;     // most tokens per CTA (a power of two)
+constexpr int kRopeAxesRows = 8;      // most tokens per CTA (a power of two)
 constexpr int kRopeAxesThreads = 256;
 constexpr int kRopeMaxAxes = 4;
 
