@@ -275,26 +275,6 @@ __global__ void __launch_bounds__(128, CacheAttend<NH>::kPerSm) cache_attend_ker
     const int n_tiles = static_cast<int>((blockIdx.x + 1) * total / ctas - g0);
     TilePos cur = cache_locate(cache_len, g0, B, Hk, T, S, k, lane);
 
-    if (tid == 0) {
-        for (int i = 0; i < 4; ++i) mbar_init(bars + i, 1);
-        *abort_flag = 0;
-        fence_barrier_init();
-    }
-    if (warp == 1) {
-        tmem_alloc(tmem_slot, SM::kTmemCols);
-        tmem_relinquish();
-    }
-    // rows of heads past G stay zero: logits 0, nothing of them is written
-    for (int e = tid; e < (SM::kNS + SM::kNP) * 8; e += 128)
-        *reinterpret_cast<uint4 *>(smem + SM::kQ + e * 16) = make_uint4(0u, 0u, 0u, 0u);
-    if (tid < NH) head_f[tid] = 0.f, head_m[tid] = -INFINITY, head_l[tid] = 0.f;
-    grid_dependency_wait();  // the selection (k > 0) has been written
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    grid_dependents_launch();
-    const uint32_t tmem = *tmem_slot;
-
     struct Blocks {
         int v[kPer];  // -1: none
     };
@@ -341,6 +321,16 @@ __global__ void __launch_bounds__(128, CacheAttend<NH>::kPerSm) cache_attend_ker
     };
 
     constexpr int kLoader = 96;  // the thread that issues the loads (thread 0 issues the products)
+    if (tid == kLoader) {
+        for (int i = 0; i < 4; ++i) mbar_init(bars + i, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, SM::kTmemCols);
+        tmem_relinquish();
+    }
+    grid_dependency_wait();  // the selection (k > 0) has been written
     Blocks blk = blocks_of(cur), blk1 = blk, blk2 = blk;
     int loads_k = 0, loads_v = 0, products_s = 0, products_o = 0;  // issued by this thread
     if (tid == kLoader) {
@@ -348,6 +338,10 @@ __global__ void __launch_bounds__(128, CacheAttend<NH>::kPerSm) cache_attend_ker
         load(&mapV, bar_v, SM::kTile, cur, blk);
         loads_k = loads_v = 1;
     }
+    // rows of heads past G stay zero: logits 0, nothing of them is written
+    for (int e = tid; e < (SM::kNS + SM::kNP) * 8; e += 128)
+        *reinterpret_cast<uint4 *>(smem + SM::kQ + e * 16) = make_uint4(0u, 0u, 0u, 0u);
+    if (tid < NH) head_f[tid] = 0.f, head_m[tid] = -INFINITY, head_l[tid] = 0.f;
     Scales sc = scales_of(cur, blk), sc1 = sc;
     TilePos pos1 = cur, pos2;
     if (n_tiles > 1) {
@@ -355,6 +349,11 @@ __global__ void __launch_bounds__(128, CacheAttend<NH>::kPerSm) cache_attend_ker
         blk1 = blocks_of(pos1);
     }
     pos2 = pos1;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    grid_dependents_launch();
+    const uint32_t tmem = *tmem_slot;
     auto leave = [&](bool failed) {
         if (failed) {  // let the loads and products in flight finish
             if (loads_k) mbar_drain(bar_k, (loads_k - 1) & 1);
@@ -672,8 +671,11 @@ struct CachePartials {
 // The CTAs c with tiles of a pair: c * total / ctas <= tile < (c + 1) * total / ctas.
 __device__ __forceinline__ CachePartials cache_partials_of(int64_t total, int64_t first, int nt, int grid, int bh) {
     const int64_t ctas = min(static_cast<int64_t>(grid), total);
-    const int c0 = static_cast<int>(((first + 1) * ctas - 1) / total);
-    const int c1 = static_cast<int>(((first + nt) * ctas - 1) / total);
+    // (quotients of integers below 2^53 by one below 2^31 round down correctly in fp64, at a fraction of the
+    // cost of a 64-bit division)
+    const double per = static_cast<double>(total);
+    const int c0 = static_cast<int>(static_cast<double>((first + 1) * ctas - 1) / per);
+    const int c1 = static_cast<int>(static_cast<double>((first + nt) * ctas - 1) / per);
     return CachePartials{c1 - c0 + 1, static_cast<size_t>(c0) + bh};
 }
 

@@ -13,9 +13,10 @@
 // error of the order of fp32's own rounding at any 32-bit position.
 //
 // One CTA per `rows` consecutive tokens (flattened over the sequences) and
-// slice of heads: the tokens' cosines and sines are computed once.  A thread
-// keeps those of one token's 16-byte piece in registers and walks down the
-// heads with them, four heads' loads (both halves of the row) in flight.
+// slice of heads: the tokens' cosines and sines are computed once, while the
+// first heads' rows are on their way.  A thread keeps those of one token's
+// 16-byte piece in registers and walks down the heads with them, four heads'
+// loads (both halves of the row) in flight.
 // HBM-bound: one read and one write of the tensors.
 #pragma once
 
@@ -68,49 +69,41 @@ __device__ __forceinline__ uint4 rope_pack(const float (&v)[16 / sizeof(T)]) {
     return make_uint4(p[0], p[1], p[2], p[3]);
 }
 
-// One token's piece of heads h, h + step, .. below h1 of one tensor, from `in` to `out` (this piece of head 0).
-// They may be the same: a thread reads both halves of a row before it writes them, and no other thread
-// touches them.
-template <typename T>
-__device__ __forceinline__ void rope_axes_heads(const RopeAxesTensor &X, const T *in, T *out, int h, int h1, int step,
-                                                int half, const float2 (&cs)[16 / sizeof(T)]) {
-    constexpr int V = 16 / sizeof(T), U = 4;
-    for (; h < h1; h += U * step) {
-        uint4 a[U], c[U];
-#pragma unroll
-        for (int i = 0; i < U; ++i)
-            if (h + i * step < h1) {
-                const T *x = in + (h + i * step) * X.is[1];
-                a[i] = *reinterpret_cast<const uint4 *>(x);
-                c[i] = *reinterpret_cast<const uint4 *>(x + half);
-            }
-#pragma unroll
-        for (int i = 0; i < U; ++i)
-            if (h + i * step < h1) {
-                float x0[V], x1[V], y0[V], y1[V];
-                rope_unpack<T>(a[i], x0);
-                rope_unpack<T>(c[i], x1);
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    y0[v] = x0[v] * cs[v].x - x1[v] * cs[v].y;
-                    y1[v] = x0[v] * cs[v].y + x1[v] * cs[v].x;
-                }
-                T *y = out + (h + i * step) * X.os[1];
-                *reinterpret_cast<uint4 *>(y) = rope_pack<T>(y0);
-                *reinterpret_cast<uint4 *>(y + half) = rope_pack<T>(y1);
-            }
-    }
-}
-
 // grid (ceil(B*T / rows), head slices); heads_per = query heads, then key heads, of one slice.
 template <typename T>
 __global__ void __launch_bounds__(kRopeAxesThreads, 3) rope_axes_kernel(
     const __grid_constant__ RopeAxesTable tab, const int32_t *__restrict__ pos, int64_t BT, int T_len, int half,
     int rows, int heads_per, float sign, const __grid_constant__ RopeAxesTensor Q,
     const __grid_constant__ RopeAxesTensor K) {
+    constexpr int V = 16 / sizeof(T), U = 4;
     __shared__ float2 cs[kRopeAxesRows][64];
     const int64_t f0 = static_cast<int64_t>(blockIdx.x) * rows;
     const int nt = static_cast<int>(min(static_cast<int64_t>(rows), BT - f0));
+    // thread: 16-byte piece u of token tt, heads h, h + step, .. (rows * units divides the CTA); the queries'
+    // heads come first, then the keys'
+    const int units = half / V, u = threadIdx.x % units, tt = threadIdx.x / units % rows;
+    const int step = kRopeAxesThreads / units / rows;
+    const int h1 = min((static_cast<int>(blockIdx.y) + 1) * heads_per, Q.heads + K.heads);
+    int h = blockIdx.y * heads_per + threadIdx.x / units / rows;
+    if (tt >= nt) h = h1;
+    const int64_t f = f0 + tt, b = f / T_len, t = f % T_len;
+    const T *q_in = static_cast<const T *>(Q.in) + b * Q.is[0] + t * Q.is[2] + u * V;
+    const T *k_in = static_cast<const T *>(K.in) + b * K.is[0] + t * K.is[2] + u * V;
+    // The outputs may be the inputs: a thread reads both halves of a row before it writes them, and no other
+    // thread touches them.
+    uint4 a[U], c[U];
+    auto load = [&]() {
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int hi = h + i * step;
+            if (hi < h1) {
+                const T *x = hi < Q.heads ? q_in + hi * Q.is[1] : k_in + (hi - Q.heads) * K.is[1];
+                a[i] = *reinterpret_cast<const uint4 *>(x);
+                c[i] = *reinterpret_cast<const uint4 *>(x + half);
+            }
+        }
+    };
+    load();
     for (int e = threadIdx.x; e < nt * half; e += kRopeAxesThreads) {
         const int tt = e / half, i = e % half;
         const double p = static_cast<double>(__ldg(pos + tab.axis[i] * BT + f0 + tt));
@@ -122,24 +115,33 @@ __global__ void __launch_bounds__(kRopeAxesThreads, 3) rope_axes_kernel(
         cs[tt][i] = make_float2(fmaf(-e1, s, c), sign * fmaf(e1, c, s));
     }
     __syncthreads();
-    // thread: 16-byte piece u of token tt, heads hg, hg + step, .. (rows * units divides the CTA)
-    constexpr int V = 16 / sizeof(T);
-    const int units = half / V, u = threadIdx.x % units, tt = threadIdx.x / units % rows;
-    const int hg = threadIdx.x / units / rows, step = kRopeAxesThreads / units / rows;
     if (tt >= nt) return;
     float2 mine[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) mine[v] = cs[tt][u * V + v];
-    const int64_t f = f0 + tt, b = f / T_len, t = f % T_len;
-    const int h0 = blockIdx.y * heads_per, h1 = min(h0 + heads_per, Q.heads + K.heads);
-    if (h0 < Q.heads)
-        rope_axes_heads<T>(Q, static_cast<const T *>(Q.in) + b * Q.is[0] + t * Q.is[2] + u * V,
-                           static_cast<T *>(Q.out) + b * Q.os[0] + t * Q.os[2] + u * V, h0 + hg, min(h1, Q.heads), step,
-                           half, mine);
-    if (h1 > Q.heads)
-        rope_axes_heads<T>(K, static_cast<const T *>(K.in) + b * K.is[0] + t * K.is[2] + u * V,
-                           static_cast<T *>(K.out) + b * K.os[0] + t * K.os[2] + u * V, max(h0 - Q.heads, 0) + hg,
-                           h1 - Q.heads, step, half, mine);
+    T *q_out = static_cast<T *>(Q.out) + b * Q.os[0] + t * Q.os[2] + u * V;
+    T *k_out = static_cast<T *>(K.out) + b * K.os[0] + t * K.os[2] + u * V;
+    while (h < h1) {
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int hi = h + i * step;
+            if (hi < h1) {
+                float x0[V], x1[V], y0[V], y1[V];
+                rope_unpack<T>(a[i], x0);
+                rope_unpack<T>(c[i], x1);
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    y0[v] = x0[v] * mine[v].x - x1[v] * mine[v].y;
+                    y1[v] = x0[v] * mine[v].y + x1[v] * mine[v].x;
+                }
+                T *y = hi < Q.heads ? q_out + hi * Q.os[1] : k_out + (hi - Q.heads) * K.os[1];
+                *reinterpret_cast<uint4 *>(y) = rope_pack<T>(y0);
+                *reinterpret_cast<uint4 *>(y + half) = rope_pack<T>(y1);
+            }
+        }
+        h += U * step;
+        load();
+    }
 }
 
 }  // namespace ssa
