@@ -215,7 +215,7 @@ struct CacheAttend {
     static constexpr int kNS = NH < 8 ? 16 : 2 * NH;                 // columns of the logits' product (term * NH + head)
     static constexpr int kNP = (3 * NH + 15) / 16 * 16;              // columns of the output's product
     static constexpr int kQ = 2 * kTile;                             // [kNS][128 B]
-    static constexpr int kP = kQ + kNS * 128;                        // [kNP][128 B]
+    static constexpr int kP = kQ + kNS * 128;                        // [kNP / 16][128 keys][16 B]
     static constexpr int kRed = kP + kNP * 128;                      // two of: [NH][4 warps] maxima, [NH][4 warps] sums
     static constexpr int kHead = kRed + 2 * 2 * NH * 16;             // [NH] logit factor, [NH] maximum, [NH] sum
     static constexpr int kBar = kHead + 3 * NH * 4;
@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(128, CacheAttend<NH>::kPerSm) cache_attend_ker
         loads_k = loads_v = 1;
     }
     // rows of heads past G stay zero: logits 0, nothing of them is written
-    for (int e = tid; e < (SM::kNS + SM::kNP) * 8; e += 128)
+    for (int e = tid; e < SM::kNS * 8; e += 128)
         *reinterpret_cast<uint4 *>(smem + SM::kQ + e * 16) = make_uint4(0u, 0u, 0u, 0u);
     if (tid < NH) head_f[tid] = 0.f, head_m[tid] = -INFINITY, head_l[tid] = 0.f;
     Scales sc = scales_of(cur, blk), sc1 = sc;
@@ -529,28 +529,31 @@ __global__ void __launch_bounds__(128, CacheAttend<NH>::kPerSm) cache_attend_ker
             constexpr int kLanes = 32 / NH;  // lanes that end up with the same head
             if (lane % kLanes == 0) red_l[lane / kLanes * 4 + warp] = sum[0];
         }
-        // three terms of every weight into the K-major operand: row term * NH + h, byte = key
+        // three terms of every weight into the N-major operand: byte term * NH + h of the key's row, rows of 16
+        // bytes in groups of 2 KB (one 16-byte store per 16 bytes; key by key, single bytes would go to rows of
+        // their own)
         {
-            uint8_t *base = smem + SM::kP + (tid & 15);
-            const int u16 = tid >> 4;
-            auto put = [&](int row, uint32_t byte) {
-                base[row * 128 + ((u16 ^ (row & 7)) << 4)] = static_cast<uint8_t>(byte);
-            };
+            uint32_t w[SM::kNP / 4];
+#pragma unroll
+            for (int i = 0; i < SM::kNP / 4; ++i) w[i] = 0u;
 #pragma unroll
             for (int h = 0; h < NH; h += 2) {
                 float a = p[h], c = p[h + 1];
 #pragma unroll
                 for (int term = 0; term < 3; ++term) {
-                    const uint16_t w = pack_e4m3x2(a, c);
-                    put(term * NH + h, w & 0xFFu);
-                    put(term * NH + h + 1, w >> 8);
+                    const uint16_t e = pack_e4m3x2(a, c);
+                    w[(term * NH + h) / 4] |= static_cast<uint32_t>(e) << (h % 4 * 8);
                     if (term < 2) {
-                        const float2 f = unpack_e4m3x2(w);
+                        const float2 f = unpack_e4m3x2(e);
                         a = (a - f.x) * 16.f;
                         c = (c - f.y) * 16.f;
                     }
                 }
             }
+#pragma unroll
+            for (int g = 0; g < SM::kNP / 16; ++g)
+                *reinterpret_cast<uint4 *>(smem + SM::kP + g * 2048 + tid * 16) =
+                    make_uint4(w[4 * g], w[4 * g + 1], w[4 * g + 2], w[4 * g + 3]);
         }
         ok = ok && mbar_wait(bar_v, ph, abort_flag, 0x713);
         if (ok && !valid) {  // whatever the cache holds behind the newest token must not meet even a weight of 0
@@ -566,10 +569,10 @@ __global__ void __launch_bounds__(128, CacheAttend<NH>::kPerSm) cache_attend_ker
         }
         if (tid == 0) {
             tc_fence_after();
-            constexpr uint32_t id = idesc_e4m3(128, SM::kNP, true, false);
+            constexpr uint32_t id = idesc_e4m3(128, SM::kNP, true, true);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-                mma_e4m3_ss(tmem + SM::kTmemO, smem_desc_sw128(sV + kk * 4096, 16), smem_desc_sw128(sP + kk * 32, 16),
+                mma_e4m3_ss(tmem + SM::kTmemO, smem_desc_sw128(sV + kk * 4096, 16), smem_desc_mn8(sP + kk * 512, 128, 2048),
                             id, kk > 0 ? 1u : 0u);
             mma_commit(bar_o);
             ++products_o;

@@ -346,6 +346,18 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr, uint32_t lbo
     return d;
 }
 
+// Shared-memory matrix descriptor without swizzle, MN-major 8-bit operand: core matrices of 8 K rows x 16 M/N
+// bytes, 128 contiguous bytes each; lbo = bytes from one group of 8 K rows to the next, sbo = bytes from one
+// group of 16 M/N elements to the next.
+__device__ __forceinline__ uint64_t smem_desc_mn8(uint32_t saddr, uint32_t lbo_bytes, uint32_t sbo_bytes) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+    d |= static_cast<uint64_t>((lbo_bytes >> 4) & 0x3FFFu) << 16;
+    d |= static_cast<uint64_t>((sbo_bytes >> 4) & 0x3FFFu) << 32;
+    d |= static_cast<uint64_t>(1) << 46;  // descriptor version (sm100)
+    return d;
+}
+
 // tcgen05.ld / st, 32 lanes x 32 bit, 32 consecutive columns per thread.
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
     uint32_t r[32];
