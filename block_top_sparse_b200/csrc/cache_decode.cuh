@@ -216,9 +216,9 @@ struct CacheAttend {
     static constexpr int kNP = (3 * NH + 15) / 16 * 16;              // columns of the output's product
     static constexpr int kQ = 2 * kTile;                             // [kNS][128 B]
     static constexpr int kP = kQ + kNS * 128;                        // [kNP / 16][128 keys][16 B]
-    static constexpr int kRed = kP + kNP * 128;                      // two of: [NH][4 warps] maxima, [NH][4 warps] sums
-    static constexpr int kHead = kRed + 2 * 2 * NH * 16;             // [NH] logit factor, [NH] maximum, [NH] sum
-    static constexpr int kBar = kHead + 3 * NH * 4;
+    static constexpr int kRed = kP + kNP * 128;                      // two of: [NH][4 warps] sums
+    static constexpr int kHead = kRed + 2 * NH * 16;                 // [NH] logit factor, [2][NH] maximum, [NH] sum
+    static constexpr int kBar = kHead + 4 * NH * 4;
     static constexpr int kBytes = kBar + 64 + 1024;                  // + alignment of the dynamic base to 1024 B
     // the logits' columns may be written again while the outputs are read, except at NH = 32, where both
     // products would take 256 columns a CTA and the outputs take the logits' place
@@ -253,7 +253,10 @@ __global__ void __launch_bounds__(128, CacheAttend<NH>::kPerSm) cache_attend_ker
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(cad_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t sK = smem_u32(smem), sV = sK + SM::kTile, sQ = sK + SM::kQ, sP = sK + SM::kP;
-    float *head_f = reinterpret_cast<float *>(smem + SM::kHead), *head_m = head_f + NH, *head_l = head_m + NH;
+    float *head_f = reinterpret_cast<float *>(smem + SM::kHead), *head_m = head_f + NH, *head_l = head_m + 2 * NH;
+    // running maximum of a head before any key: below every finite logit, so that a masked or overflowing one
+    // (-inf) weighs 0
+    constexpr float kLowest = -3.4e38f;
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + SM::kBar);
     uint64_t *bar_k = bars, *bar_v = bars + 1, *bar_s = bars + 2, *bar_o = bars + 3;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 4);
@@ -341,7 +344,7 @@ __global__ void __launch_bounds__(128, CacheAttend<NH>::kPerSm) cache_attend_ker
     // rows of heads past G stay zero: logits 0, nothing of them is written
     for (int e = tid; e < SM::kNS * 8; e += 128)
         *reinterpret_cast<uint4 *>(smem + SM::kQ + e * 16) = make_uint4(0u, 0u, 0u, 0u);
-    if (tid < NH) head_f[tid] = 0.f, head_m[tid] = -INFINITY, head_l[tid] = 0.f;
+    if (tid < NH) head_f[tid] = 0.f, head_m[tid] = head_m[NH + tid] = kLowest, head_l[tid] = 0.f;
     Scales sc = scales_of(cur, blk), sc1 = sc;
     TilePos pos1 = cur, pos2;
     if (n_tiles > 1) {
@@ -388,7 +391,7 @@ __global__ void __launch_bounds__(128, CacheAttend<NH>::kPerSm) cache_attend_ker
     };
     if (NH <= 16) load_q(cur.b * Hk + cur.hk);
 
-    float o[NH];
+    uint64_t o[NH / 2];  // outputs of heads 2 i and 2 i + 1, this thread's dim
     int pair = -1;
     for (int it = 0; it < n_tiles; ++it) {
         const uint32_t ph = it & 1;
@@ -432,12 +435,12 @@ __global__ void __launch_bounds__(128, CacheAttend<NH>::kPerSm) cache_attend_ker
                 if (lane == 0) {
                     // an infinity or NaN in the query makes the row's results NaN, not large
                     head_f[h] = finite ? unit * scale_log2 : __int_as_float(0x7FC00000);
-                    head_m[h] = -INFINITY;
+                    head_m[h] = head_m[NH + h] = kLowest;
                     head_l[h] = 0.f;
                 }
             }
 #pragma unroll
-            for (int h = 0; h < NH; ++h) o[h] = 0.f;
+            for (int i = 0; i < NH / 2; ++i) o[i] = 0;
             fence_proxy_async_smem();
             __syncthreads();
         }
@@ -455,59 +458,81 @@ __global__ void __launch_bounds__(128, CacheAttend<NH>::kPerSm) cache_attend_ker
         }
         const int my_blk = kPer == 1 ? blk.v[0] : (tid < S ? blk.v[0] : blk.v[kPer - 1]);
         const bool valid = my_blk >= 0 && my_blk * S + tid % S <= cur.L;
-        float *red_m = reinterpret_cast<float *>(smem + SM::kRed + (it & 1) * 2 * NH * 16), *red_l = red_m + NH * 4;
-        float p[NH];
+        float *red_l = reinterpret_cast<float *>(smem + SM::kRed + (it & 1) * NH * 16);
+        // Maxima before (old) and with (now) this tile.  They change places tile by tile, so that warps may raise
+        // those of the next tile while others still read these.
+        float *now_m = head_m + (it & 1 ? 0 : NH), *old_m = head_m + (it & 1 ? NH : 0);
+        uint64_t p[NH / 2];  // logits, then weights, of heads 2 i and 2 i + 1
         {
             const uint32_t row = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+            const uint64_t sixteenth = f2_pack(0.0625f, 0.0625f);
+            auto join = [&](const float *t0, const float *t1) {
+#pragma unroll
+                for (int i = 0; i < NH / 2; ++i)
+                    p[i] = ffma2(f2_pack(t1[2 * i], t1[2 * i + 1]), sixteenth, f2_pack(t0[2 * i], t0[2 * i + 1]));
+            };
             if constexpr (NH <= 8) {
                 float v[16];
                 tmem_ld16(row, v);
-#pragma unroll
-                for (int h = 0; h < NH; ++h) p[h] = fmaf(v[NH + h], 0.0625f, v[h]);
+                join(v, v + NH);
             } else if constexpr (NH == 16) {
                 float v[32];
                 tmem_ld32(row, v);
-#pragma unroll
-                for (int h = 0; h < 16; ++h) p[h] = fmaf(v[16 + h], 0.0625f, v[h]);
+                join(v, v + 16);
             } else {
-                float v[32];
-                tmem_ld32(row, p);
-                tmem_ld32(row + 32, v);
-#pragma unroll
-                for (int h = 0; h < 32; ++h) p[h] = fmaf(v[h], 0.0625f, p[h]);
+                float v[32], w[32];
+                tmem_ld32(row, v);
+                tmem_ld32(row + 32, w);
+                join(v, w);
             }
         }
+        {
+            const uint64_t kk = f2_pack(sc.k, sc.k);
+            float mine = 0.f;  // the warp's maximum of head `lane`
 #pragma unroll
-        for (int h = 0; h < NH; ++h) {
-            p[h] = valid ? p[h] * (sc.k * head_f[h]) : -INFINITY;
-            float m;
-            asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(p[h]));
-            if (lane == 0) red_m[h * 4 + warp] = m;
+            for (int i = 0; i < NH / 2; ++i) {
+                p[i] = fmul2(p[i], fmul2(kk, *reinterpret_cast<const uint64_t *>(head_f + 2 * i)));
+                float a, c, ma, mc;
+                f2_unpack(p[i], a, c);
+                a = valid ? a : -INFINITY;
+                c = valid ? c : -INFINITY;
+                p[i] = f2_pack(a, c);
+                asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(ma) : "f"(a));
+                asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(mc) : "f"(c));
+                mine = lane == 2 * i ? ma : lane == 2 * i + 1 ? mc : mine;
+            }
+            if (lane < NH) atomic_max_shared(now_m + lane, mine);
         }
         tc_fence_before();
         __syncthreads();
         // weights against the new maximum, in units of 1/256 of the tile's largest value scale
         float sum[NH];
         bool grown = false;
+        const float head_old = tid < NH ? old_m[tid] : 0.f;  // (behind the next barrier others raise it)
         const float unit = kPer == 1 ? 256.f : (sc.top > 0.f ? 256.f * (sc.v / sc.top) : 0.f);  // powers of two
+        {
+            const uint64_t unit2 = f2_pack(unit, unit);
 #pragma unroll
-        for (int h = 0; h < NH; ++h) {
-            const float4 r = *reinterpret_cast<const float4 *>(red_m + h * 4);
-            const float old = head_m[h];
-            float m = fmaxf(fmaxf(fmaxf(r.x, r.y), fmaxf(r.z, r.w)), old);
-            if (m == -INFINITY) m = 0.f;  // only overflowing logits: weights 0
-            grown |= m != old;
-            sum[h] = fast_exp2(p[h] - m);  // 0 for a masked key
-            p[h] = sum[h] * unit;
+            for (int i = 0; i < NH / 4; ++i) {
+                const float4 m = *reinterpret_cast<const float4 *>(now_m + 4 * i);
+                const float4 old = *reinterpret_cast<const float4 *>(old_m + 4 * i);
+                grown |= m.x != old.x || m.y != old.y || m.z != old.z || m.w != old.w;
+                float a[4];
+                f2_unpack(fadd2(p[2 * i], f2_pack(-m.x, -m.y)), a[0], a[1]);
+                f2_unpack(fadd2(p[2 * i + 1], f2_pack(-m.z, -m.w)), a[2], a[3]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sum[4 * i + e] = fast_exp2(a[e]);  // 0 for a masked key
+                p[2 * i] = fmul2(f2_pack(sum[4 * i], sum[4 * i + 1]), unit2);
+                p[2 * i + 1] = fmul2(f2_pack(sum[4 * i + 2], sum[4 * i + 3]), unit2);
+            }
         }
         if (grown) {  // (uniform) the outputs so far are brought to the new maxima
 #pragma unroll
-            for (int h = 0; h < NH; ++h) {
-                const float4 r = *reinterpret_cast<const float4 *>(red_m + h * 4);
-                const float old = head_m[h];
-                float m = fmaxf(fmaxf(fmaxf(r.x, r.y), fmaxf(r.z, r.w)), old);
-                if (m == -INFINITY) m = 0.f;
-                o[h] *= m != old ? fast_exp2(old - m) : 1.f;
+            for (int i = 0; i < NH / 4; ++i) {
+                const float4 m = *reinterpret_cast<const float4 *>(now_m + 4 * i);
+                const float4 old = *reinterpret_cast<const float4 *>(old_m + 4 * i);
+                o[2 * i] = fmul2(o[2 * i], f2_pack(fast_exp2(old.x - m.x), fast_exp2(old.y - m.y)));
+                o[2 * i + 1] = fmul2(o[2 * i + 1], f2_pack(fast_exp2(old.z - m.z), fast_exp2(old.w - m.w)));
             }
         }
         // sums over the warp: each step hands a lane half of the heads it holds
@@ -538,16 +563,15 @@ __global__ void __launch_bounds__(128, CacheAttend<NH>::kPerSm) cache_attend_ker
             for (int i = 0; i < SM::kNP / 4; ++i) w[i] = 0u;
 #pragma unroll
             for (int h = 0; h < NH; h += 2) {
-                float a = p[h], c = p[h + 1];
+                uint64_t rest = p[h / 2];
 #pragma unroll
                 for (int term = 0; term < 3; ++term) {
+                    float a, c;
+                    f2_unpack(rest, a, c);
                     const uint16_t e = pack_e4m3x2(a, c);
                     w[(term * NH + h) / 4] |= static_cast<uint32_t>(e) << (h % 4 * 8);
-                    if (term < 2) {
-                        const float2 f = unpack_e4m3x2(e);
-                        a = (a - f.x) * 16.f;
-                        c = (c - f.y) * 16.f;
-                    }
+                    // 16 (rest - e), exact
+                    if (term < 2) rest = ffma2(unpack_e4m3x2_f2(e), f2_pack(-16.f, -16.f), fmul2(rest, f2_pack(16.f, 16.f)));
                 }
             }
 #pragma unroll
@@ -581,14 +605,11 @@ __global__ void __launch_bounds__(128, CacheAttend<NH>::kPerSm) cache_attend_ker
         }
         // meanwhile: the head's running maximum and sum, and the blocks' own
         if (tid < NH) {
-            const float4 rm = *reinterpret_cast<const float4 *>(red_m + tid * 4);
             const float4 rl = *reinterpret_cast<const float4 *>(red_l + tid * 4);
-            const float old = head_m[tid];
-            float m = fmaxf(fmaxf(fmaxf(rm.x, rm.y), fmaxf(rm.z, rm.w)), old);
-            if (m == -INFINITY) m = 0.f;
-            const float l = (rl.x + rl.y) + (rl.z + rl.w);
-            head_l[tid] = head_l[tid] * (m != old ? fast_exp2(old - m) : 1.f) + l;
-            head_m[tid] = m;
+            const float m = now_m[tid], l = (rl.x + rl.y) + (rl.z + rl.w);
+            head_l[tid] = head_l[tid] * fast_exp2(head_old - m) + l;
+            // the next tile's maxima start from these; others may have begun to raise them
+            atomic_max_shared(old_m + tid, m);
             if (block_ml && tid < G) {
                 float2 *to = block_ml + (static_cast<size_t>(bh) * G + tid) * (k > 0 ? k : nb) + cur.t * kPer;
                 if (kPer == 1) {
@@ -608,30 +629,36 @@ __global__ void __launch_bounds__(128, CacheAttend<NH>::kPerSm) cache_attend_ker
         {
             const uint32_t row = tmem + SM::kTmemO + (static_cast<uint32_t>(warp * 32) << 16);
             const float back = sc.top * (1.f / 256.f);
+            const uint64_t back2 = f2_pack(back, back), sixteenth = f2_pack(0.0625f, 0.0625f);
+            auto add = [&](const float *t0, const float *t1, const float *t2) {
+#pragma unroll
+                for (int i = 0; i < NH / 2; ++i) {
+                    const uint64_t a = ffma2(f2_pack(t2[2 * i], t2[2 * i + 1]), sixteenth, f2_pack(t1[2 * i], t1[2 * i + 1]));
+                    o[i] = ffma2(ffma2(a, sixteenth, f2_pack(t0[2 * i], t0[2 * i + 1])), back2, o[i]);
+                }
+            };
             if constexpr (NH == 4) {
                 float v[16];
                 tmem_ld16(row, v);
-#pragma unroll
-                for (int h = 0; h < 4; ++h) o[h] = fmaf(fmaf(fmaf(v[8 + h], 0.0625f, v[4 + h]), 0.0625f, v[h]), back, o[h]);
+                add(v, v + 4, v + 8);
             } else if constexpr (NH == 8) {
                 float v[32];
                 tmem_ld32(row, v);
-#pragma unroll
-                for (int h = 0; h < 8; ++h) o[h] = fmaf(fmaf(fmaf(v[16 + h], 0.0625f, v[8 + h]), 0.0625f, v[h]), back, o[h]);
+                add(v, v + 8, v + 16);
             } else if constexpr (NH == 16) {
                 float v[32], w[16];
                 tmem_ld32(row, v);
                 tmem_ld16(row + 32, w);
-#pragma unroll
-                for (int h = 0; h < 16; ++h) o[h] = fmaf(fmaf(fmaf(w[h], 0.0625f, v[16 + h]), 0.0625f, v[h]), back, o[h]);
+                add(v, v + 16, w);
             } else {
                 float f = back;
 #pragma unroll
                 for (int term = 0; term < 3; ++term, f *= 0.0625f) {
                     float v[32];
                     tmem_ld32(row + 32 * term, v);
+                    const uint64_t f2 = f2_pack(f, f);
 #pragma unroll
-                    for (int h = 0; h < 32; ++h) o[h] = fmaf(v[h], f, o[h]);
+                    for (int i = 0; i < 16; ++i) o[i] = ffma2(f2_pack(v[2 * i], v[2 * i + 1]), f2, o[i]);
                 }
             }
             tc_fence_before();
@@ -644,9 +671,13 @@ __global__ void __launch_bounds__(128, CacheAttend<NH>::kPerSm) cache_attend_ker
             const size_t slot = static_cast<size_t>(blockIdx.x) + bh;
             float *to = opart + slot * G * kCacheD + tid;
 #pragma unroll
-            for (int h = 0; h < NH; ++h)
-                if (h < G) to[h * kCacheD] = o[h];
-            if (tid < G) mlpart[slot * G + tid] = make_float2(head_m[tid], head_l[tid]);
+            for (int i = 0; i < NH / 2; ++i) {
+                float a, c;
+                f2_unpack(o[i], a, c);
+                if (2 * i < G) to[2 * i * kCacheD] = a;
+                if (2 * i + 1 < G) to[(2 * i + 1) * kCacheD] = c;
+            }
+            if (tid < G) mlpart[slot * G + tid] = make_float2(now_m[tid], head_l[tid]);
             __syncthreads();  // head_* are set anew for the next pair
         } else if (!SM::kApart) {
             __syncthreads();  // every warp has read its outputs before the next logits take their place

@@ -512,6 +512,22 @@ __device__ __forceinline__ float2 unpack_e4m3x2(uint16_t v) {
     return __half22float2(*reinterpret_cast<__half2 *>(&h));
 }
 
+// Two e4m3 codes as a packed pair of floats.
+__device__ __forceinline__ uint64_t unpack_e4m3x2_f2(uint16_t v) {
+    const float2 f = unpack_e4m3x2(v);
+    return f2_pack(f.x, f.y);
+}
+
+// Raises a float in shared memory to v, in whatever order several threads come: as integers, floats >= 0 grow
+// with their value and negative ones fall (+ 0.f: -0 counts as 0).
+__device__ __forceinline__ void atomic_max_shared(float *to, float v) {
+    v += 0.f;
+    if (v >= 0.f)
+        atomicMax(reinterpret_cast<int *>(to), __float_as_int(v));
+    else
+        atomicMin(reinterpret_cast<unsigned *>(to), __float_as_uint(v));
+}
+
 // Programmatic dependent launch: wait until the kernels this one depends on have completed and their writes
 // are visible (returns at once for a kernel launched without the attribute); let the dependent kernel's
 // CTAs start while this kernel still runs.
