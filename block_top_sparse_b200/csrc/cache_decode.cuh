@@ -249,6 +249,7 @@ __global__ void __launch_bounds__(128, CacheAttend<NH>::kPerSm) cache_attend_ker
     float2 *__restrict__ block_ml, int B, int Hk, int G, int T, int k, int nb, float scale_log2) {
     using SM = CacheAttend<NH>;
     constexpr int kPer = 128 / S;  // blocks of a tile
+    grid_dependents_launch();      // (takes effect once every CTA of this grid has started)
     extern __shared__ __align__(1024) uint8_t cad_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(cad_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -355,7 +356,6 @@ __global__ void __launch_bounds__(128, CacheAttend<NH>::kPerSm) cache_attend_ker
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    grid_dependents_launch();
     const uint32_t tmem = *tmem_slot;
     auto leave = [&](bool failed) {
         if (failed) {  // let the loads and products in flight finish
@@ -760,10 +760,28 @@ __global__ void __launch_bounds__(256) cache_combine_kernel(const int32_t *__res
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
         float2 t = make_float2(-INFINITY, 0.f);
         if (mine && nt > 0) {
-            t = cache_join(ml, P.n, G, h, lane);
             const float4 *op = reinterpret_cast<const float4 *>(opart + (P.slot0 * G + h) * kCacheD) + lane;
+            constexpr int U = 4;  // the first outputs are asked for along with the maxima
+            float4 v0[U];
+            float m0[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int i = grp + u * WPH;
+                if (i < P.n) {
+                    v0[u] = __ldcg(op + static_cast<size_t>(i) * G * (kCacheD / 4));
+                    m0[u] = __ldcg(ml + static_cast<size_t>(i) * G + h).x;
+                }
+            }
+            t = cache_join(ml, P.n, G, h, lane);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (grp + u * WPH < P.n) {
+                    const float f = fast_exp2(m0[u] - t.x);
+                    a.x = fmaf(f, v0[u].x, a.x), a.y = fmaf(f, v0[u].y, a.y);
+                    a.z = fmaf(f, v0[u].z, a.z), a.w = fmaf(f, v0[u].w, a.w);
+                }
 #pragma unroll 8
-            for (int i = grp; i < P.n; i += WPH) {
+            for (int i = grp + U * WPH; i < P.n; i += WPH) {
                 const float f = fast_exp2(__ldcg(ml + static_cast<size_t>(i) * G + h).x - t.x);
                 const float4 v = __ldcg(op + static_cast<size_t>(i) * G * (kCacheD / 4));
                 a.x = fmaf(f, v.x, a.x), a.y = fmaf(f, v.y, a.y), a.z = fmaf(f, v.z, a.z), a.w = fmaf(f, v.w, a.w);

@@ -997,9 +997,11 @@ ssa_status_t ssa_cache_decode(const ssa_dims_t *dims, const int32_t *cache_len, 
     if (S.k > 0)
         cache_select_kernel<<<bhk, kTopThreads, static_cast<size_t>(S.nb) * 4, st>>>(cache_len, qb, Kbar, idx, S.Hk, S.G,
                                                                                     S.T, S.s, S.k, S.nb);
+    // no more CTAs than the caches can have tiles
+    const size_t most = S.BHk * ((static_cast<size_t>(S.k > 0 ? S.k : S.nb) * S.s + 127) / 128);
+    const unsigned grid = static_cast<unsigned>(most < cache_grid(S.G) ? most : cache_grid(S.G));
     auto attend = [&](auto kernel, size_t smem) {
         if (!set_smem(kernel, smem)) return false;
-        const dim3 grid(cache_grid(S.G));
         const float scale_log2 = static_cast<float>(S.scale * 1.4426950408889634);
         if (S.k > 0)
             return launch_dependent(kernel, grid, 128, smem, st, tmK, tmV, cache_len, qb, Kscale, Vscale, idx, opart, ml,
@@ -1020,7 +1022,6 @@ ssa_status_t ssa_cache_decode(const ssa_dims_t *dims, const int32_t *cache_len, 
                                : heads(std::integral_constant<int, 32>());
     if (!ok) return SSA_ERR_CUDA;
     // partials per pair: about grid / pairs, each of 128 values per head
-    const unsigned grid = cache_grid(S.G);
     const bool wide = grid / bhk >= 16;
     const unsigned rows = static_cast<unsigned>(S.BH), head_ctas = wide ? rows : (rows + 7) / 8;
     const size_t weight_ctas = weight_out ? S.BHk * ((S.nb + 255) / 256) : 0;
