@@ -32,6 +32,8 @@
 // No atomics: results are the same from run to run.
 #pragma once
 
+#include <cooperative_groups.h>
+
 #include "cache8.cuh"
 #include "device.cuh"
 #include "top_blocks.cuh"
@@ -55,7 +57,8 @@ __device__ __forceinline__ int cache_tiles(int L, int T, int s, int k) {
 // ---------------------------------------------------------------------------
 // Selection
 // ---------------------------------------------------------------------------
-// Shared memory: nb keys.  k >= 1.
+// A cluster of CTAs per (sequence, key head), one where there are many pairs: the CTAs share the rows and put
+// their scores into the first one's shared memory (nb keys), which chooses.  k >= 1.
 __global__ void __launch_bounds__(kTopThreads, 4) cache_select_kernel(const int32_t *__restrict__ cache_len,
                                                                    const __nv_bfloat16 *__restrict__ q,
                                                                    const float *__restrict__ Kbar,
@@ -65,8 +68,11 @@ __global__ void __launch_bounds__(kTopThreads, 4) cache_select_kernel(const int3
     __shared__ TopScratch sc;
     __shared__ double qs[kCacheD];
     grid_dependents_launch();
-    const int bh = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    namespace cg = cooperative_groups;
+    const int parts = static_cast<int>(cg::this_cluster().num_blocks()), part_id = static_cast<int>(cg::this_cluster().block_rank());
+    const int bh = blockIdx.x / parts, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     constexpr int R = 8, kWarps = kTopThreads / 32;  // rows in flight per warp, four elements per lane
+    const int first = R * (part_id * kWarps + warp), stride = R * kWarps * parts;
     const int L = __ldg(cache_len + bh / Hk);
     int32_t *out = idx + static_cast<size_t>(bh) * k;
     // the first rows (whether they count or not) and the query are asked for before the length is known
@@ -77,7 +83,7 @@ __global__ void __launch_bounds__(kTopThreads, 4) cache_select_kernel(const int3
     };
     if (k > 1) {
 #pragma unroll
-        for (int i = 0; i < R; ++i) load(i, R * warp + i, nb);
+        for (int i = 0; i < R; ++i) load(i, first + i, nb);
         if (tid < kCacheD) {
             double sum = 0.0;
             const __nv_bfloat16 *qr = q + static_cast<size_t>(bh) * G * kCacheD + tid;
@@ -86,11 +92,13 @@ __global__ void __launch_bounds__(kTopThreads, 4) cache_select_kernel(const int3
             qs[tid] = sum;
         }
     }
-    if (L < 0 || L >= T) {
-        for (int i = tid; i < k; i += kTopThreads) out[i] = -1;
+    if (L < 0 || L >= T) {  // (the cluster's CTAs go the same way here and below)
+        if (part_id == 0)
+            for (int i = tid; i < k; i += kTopThreads) out[i] = -1;
         return;
     }
     const int bt = L / s, want = min(k - 1, bt);
+    if (part_id > 0 && (want == bt || want == 0)) return;
     if (want == bt) {
         for (int i = tid; i < want; i += kTopThreads) out[i] = i;
     } else if (want > 0) {
@@ -98,7 +106,8 @@ __global__ void __launch_bounds__(kTopThreads, 4) cache_select_kernel(const int3
         double q4[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) q4[i] = qs[4 * lane + i];
-        for (int j0 = R * warp; j0 < bt; j0 += R * kWarps) {
+        uint32_t *keys = parts > 1 ? cg::this_cluster().map_shared_rank(select_key, 0) : select_key;
+        for (int j0 = first; j0 < bt; j0 += stride) {
 #pragma unroll
             for (int half = 0; half < R; half += 4) {
                 double part[4];
@@ -107,7 +116,7 @@ __global__ void __launch_bounds__(kTopThreads, 4) cache_select_kernel(const int3
                     const float4 x = v[half + i];
                     part[i] = fma(q4[0], static_cast<double>(x.x), q4[1] * static_cast<double>(x.y)) +
                               fma(q4[2], static_cast<double>(x.z), q4[3] * static_cast<double>(x.w));
-                    load(half + i, j0 + half + i + R * kWarps, bt);  // the next rows arrive during the sums
+                    load(half + i, j0 + half + i + stride, bt);  // the next rows arrive during the sums
                 }
                 // butterfly: two steps hand each lane the sum of one row over 8 lanes, three more the whole sum
 #pragma unroll
@@ -122,10 +131,14 @@ __global__ void __launch_bounds__(kTopThreads, 4) cache_select_kernel(const int3
 #pragma unroll
                 for (int off = 4; off > 0; off >>= 1) part[0] += __shfl_xor_sync(0xffffffffu, part[0], off);
                 const int j = j0 + half + (lane >> 3);  // lane bit 4: row bit 1, lane bit 3: row bit 0
-                if ((lane & 7) == 0 && j < bt) select_key[j] = score_key(static_cast<float>(part[0]));
+                if ((lane & 7) == 0 && j < bt) keys[j] = score_key(static_cast<float>(part[0]));
             }
         }
-        __syncthreads();
+        if (parts > 1)
+            cg::this_cluster().sync();
+        else
+            __syncthreads();
+        if (part_id > 0) return;
         top_blocks(select_key, bt, want, out, sc);
     }
     for (int i = want + tid; i < k; i += kTopThreads) out[i] = i == want ? bt : -1;
@@ -693,9 +706,11 @@ __global__ void __launch_bounds__(128, CacheAttend<NH>::kPerSm) cache_attend_ker
 
 // ---------------------------------------------------------------------------
 // Joining the partials: M = max m_i, l = sum 2^(m_i - M) l_i, o = sum 2^(m_i - M) o_i / l, in the order of the
-// CTAs.  The first head_ctas CTAs join 8 / WPH query heads each, WPH warps per head; every CTA after them adds
-// up the attention weight of 256 blocks of one pair over its group's heads.  WPH = 8 where a pair is split over
-// many CTAs (few sequences), 1 where there are many pairs of few partials.
+// CTAs.  The first head_ctas CTAs join query heads; every CTA after them adds up the attention weight of 256
+// blocks of one pair over its group's heads.  A head CTA takes eight heads, a warp each (SPLIT = 0), where there
+// are many pairs of few partials, one head (1), or a quarter of one head's dims (4) where a pair is split over
+// many CTAs: 16 sequences of up to 32K tokens, 2 key heads, about 23 partials a pair: 38 us in all with 1 and
+// 43 us with 4; one of 131072 tokens, 1 key head, 592 partials: 27 us and 18 us.
 // ---------------------------------------------------------------------------
 struct CachePartials {
     int n;
@@ -713,26 +728,40 @@ __device__ __forceinline__ CachePartials cache_partials_of(int64_t total, int64_
     return CachePartials{c1 - c0 + 1, static_cast<size_t>(c0) + bh};
 }
 
-// Maximum and sum of one head, by one warp.
-__device__ __forceinline__ float2 cache_join(const float2 *ml, int n, int G, int h, int lane) {
+// Joins (m2, l2) into (m, l).
+__device__ __forceinline__ void cache_join(float &m, float &l, float m2, float l2) {
+    const float top = fmaxf(m, m2);
+    l = l * (m == top ? 1.f : fast_exp2(m - top)) + l2 * (m2 == top ? 1.f : fast_exp2(m2 - top));
+    m = top;
+}
+
+// Maximum and sum over n partials of one head, by `threads` threads of which this is number t (a multiple of a
+// warp); the result is that of the thread's warp alone.
+__device__ __forceinline__ float2 cache_join_partials(const float2 *ml, int n, int G, int h, int t, int threads) {
+    constexpr int U = 8;
     float m = -INFINITY, l = 0.f;
-    for (int i = lane; i < n; i += 32) {
-        const float2 a = __ldcg(ml + static_cast<size_t>(i) * G + h);
-        const float top = fmaxf(m, a.x);
-        l = l * (m == top ? 1.f : fast_exp2(m - top)) + a.y * (a.x == top ? 1.f : fast_exp2(a.x - top));
+    for (int i0 = t; i0 < n; i0 += U * threads) {
+        float2 a[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = i0 + u * threads;
+            a[u] = i < n ? __ldcg(ml + static_cast<size_t>(i) * G + h) : make_float2(-INFINITY, 0.f);
+        }
+        float top = m;
+#pragma unroll
+        for (int u = 0; u < U; ++u) top = fmaxf(top, a[u].x);
+        l *= m == top ? 1.f : fast_exp2(m - top);
+#pragma unroll
+        for (int u = 0; u < U; ++u) l += a[u].y * (a[u].x == top ? 1.f : fast_exp2(a[u].x - top));
         m = top;
     }
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-        const float m2 = __shfl_xor_sync(0xffffffffu, m, off), l2 = __shfl_xor_sync(0xffffffffu, l, off);
-        const float top = fmaxf(m, m2);
-        l = l * (m == top ? 1.f : fast_exp2(m - top)) + l2 * (m2 == top ? 1.f : fast_exp2(m2 - top));
-        m = top;
-    }
+    for (int off = 16; off > 0; off >>= 1)
+        cache_join(m, l, __shfl_xor_sync(0xffffffffu, m, off), __shfl_xor_sync(0xffffffffu, l, off));
     return make_float2(m, l);
 }
 
-template <int WPH>
+template <int SPLIT>
 __global__ void __launch_bounds__(256) cache_combine_kernel(const int32_t *__restrict__ cache_len,
                                                             const float *opart, const float2 *mlpart,
                                                             const float2 *block_ml, const int32_t *idx,
@@ -741,11 +770,10 @@ __global__ void __launch_bounds__(256) cache_combine_kernel(const int32_t *__res
                                                             int G, int T, int s, int k, int nb, int grid,
                                                             int head_ctas) {
     __shared__ float2 head[kCacheMaxGroup];
-    __shared__ float4 part[8][32];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const bool heads = static_cast<int>(blockIdx.x) < head_ctas;
     const int chunks = (nb + 255) / 256, w = blockIdx.x - head_ctas;
-    const int row = (blockIdx.x * 8 + warp) / WPH;  // query head of the batch (head CTAs)
+    const int row = SPLIT ? blockIdx.x / max(SPLIT, 1) : blockIdx.x * 8 + warp;  // query head of the batch (head CTAs)
     const int bh = heads ? min(row / G, B * Hk - 1) : w / chunks, b = bh / Hk;
     const int L = __ldg(cache_len + b), nt = cache_tiles(L, T, s, k), ns = cache_slots(L, T, s, k);
     const int64_t total = cache_total_tiles(cache_len, B, Hk, T, s, k, lane);
@@ -755,53 +783,84 @@ __global__ void __launch_bounds__(256) cache_combine_kernel(const int32_t *__res
     const float2 *ml = mlpart + P.slot0 * G;
     grid_dependency_wait();
     if (heads) {
-        const int h = row % G, grp = warp % WPH;
+        const int h = row % G;
         const bool mine = row < B * Hk * G;
+        const float4 *op = reinterpret_cast<const float4 *>(opart + (P.slot0 * G + h) * kCacheD);
+        const size_t step = static_cast<size_t>(G) * (kCacheD / 4);
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
         float2 t = make_float2(-INFINITY, 0.f);
-        if (mine && nt > 0) {
-            const float4 *op = reinterpret_cast<const float4 *>(opart + (P.slot0 * G + h) * kCacheD) + lane;
-            constexpr int U = 4;  // the first outputs are asked for along with the maxima
-            float4 v0[U];
-            float m0[U];
+        auto add = [&](float f, const float4 &v) {
+            a.x = fmaf(f, v.x, a.x), a.y = fmaf(f, v.y, a.y), a.z = fmaf(f, v.z, a.z), a.w = fmaf(f, v.w, a.w);
+        };
+        int piece = lane;       // 16 bytes of fp32 outputs
+        bool write = mine;
+        if constexpr (SPLIT == 0) {
+            if (mine && nt > 0) {
+                constexpr int U = 4;  // the first outputs are asked for along with the maxima
+                float4 v0[U];
+                float m0[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int i = grp + u * WPH;
-                if (i < P.n) {
-                    v0[u] = __ldcg(op + static_cast<size_t>(i) * G * (kCacheD / 4));
-                    m0[u] = __ldcg(ml + static_cast<size_t>(i) * G + h).x;
-                }
-            }
-            t = cache_join(ml, P.n, G, h, lane);
+                for (int u = 0; u < U; ++u)
+                    if (u < P.n) {
+                        v0[u] = __ldcg(op + u * step + lane);
+                        m0[u] = __ldcg(ml + static_cast<size_t>(u) * G + h).x;
+                    }
+                t = cache_join_partials(ml, P.n, G, h, lane, 32);
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (grp + u * WPH < P.n) {
-                    const float f = fast_exp2(m0[u] - t.x);
-                    a.x = fmaf(f, v0[u].x, a.x), a.y = fmaf(f, v0[u].y, a.y);
-                    a.z = fmaf(f, v0[u].z, a.z), a.w = fmaf(f, v0[u].w, a.w);
-                }
+                for (int u = 0; u < U; ++u)
+                    if (u < P.n) add(fast_exp2(m0[u] - t.x), v0[u]);
 #pragma unroll 8
-            for (int i = grp + U * WPH; i < P.n; i += WPH) {
-                const float f = fast_exp2(__ldcg(ml + static_cast<size_t>(i) * G + h).x - t.x);
-                const float4 v = __ldcg(op + static_cast<size_t>(i) * G * (kCacheD / 4));
-                a.x = fmaf(f, v.x, a.x), a.y = fmaf(f, v.y, a.y), a.z = fmaf(f, v.z, a.z), a.w = fmaf(f, v.w, a.w);
+                for (int i = U; i < P.n; ++i)
+                    add(fast_exp2(__ldcg(ml + static_cast<size_t>(i) * G + h).x - t.x), __ldcg(op + i * step + lane));
+            }
+        } else {
+            constexpr int kLanes = 32 / SPLIT, kGroups = 256 / kLanes;  // groups of threads take partials in turn
+            __shared__ float2 part_ml[8];
+            __shared__ float4 part_o[8][kLanes];
+            const int group = tid / kLanes;
+            piece = blockIdx.x % SPLIT * kLanes + tid % kLanes;
+            write = mine && tid < kLanes;
+            if (nt > 0) {
+                constexpr int U = 4;
+                float4 v0[U];
+                float m0[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int i = group + u * kGroups;
+                    if (i < P.n) {
+                        v0[u] = __ldcg(op + i * step + piece);
+                        m0[u] = __ldcg(ml + static_cast<size_t>(i) * G + h).x;
+                    }
+                }
+                const float2 own = cache_join_partials(ml, P.n, G, h, tid, 256);
+                if (lane == 0) part_ml[warp] = own;
+                __syncthreads();
+                t = part_ml[0];
+#pragma unroll
+                for (int i = 1; i < 8; ++i) cache_join(t.x, t.y, part_ml[i].x, part_ml[i].y);
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (group + u * kGroups < P.n) add(fast_exp2(m0[u] - t.x), v0[u]);
+#pragma unroll 8
+                for (int i = group + U * kGroups; i < P.n; i += kGroups)
+                    add(fast_exp2(__ldcg(ml + static_cast<size_t>(i) * G + h).x - t.x), __ldcg(op + i * step + piece));
+#pragma unroll
+                for (int off = kLanes; off < 32; off <<= 1) {
+                    a.x += __shfl_xor_sync(0xffffffffu, a.x, off), a.y += __shfl_xor_sync(0xffffffffu, a.y, off);
+                    a.z += __shfl_xor_sync(0xffffffffu, a.z, off), a.w += __shfl_xor_sync(0xffffffffu, a.w, off);
+                }
+                if (lane < kLanes) part_o[warp][lane] = a;
+                __syncthreads();
+                if (tid < kLanes)
+#pragma unroll
+                    for (int i = 1; i < 8; ++i) add(1.f, part_o[i][tid]);
             }
         }
-        if (WPH > 1) {
-            part[warp][lane] = a;
-            __syncthreads();
-            if (grp == 0)
-#pragma unroll
-                for (int i = 1; i < WPH; ++i) {
-                    const float4 v = part[warp + i][lane];
-                    a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
-                }
-        }
-        if (mine && grp == 0) {
+        if (write) {
             const float inv = nt > 0 ? 1.f / t.y : 0.f;  // no token (or a bad length): o = 0
-            reinterpret_cast<uint2 *>(o + static_cast<size_t>(row) * kCacheD)[lane] =
+            reinterpret_cast<uint2 *>(o + static_cast<size_t>(row) * kCacheD)[piece] =
                 make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
-            if (lane == 0) lse[row] = nt > 0 ? fmaf(t.x, kLn2, logf(t.y)) : -INFINITY;
+            if (piece == 0) lse[row] = nt > 0 ? fmaf(t.x, kLn2, logf(t.y)) : -INFINITY;
         }
         return;
     }
@@ -811,7 +870,7 @@ __global__ void __launch_bounds__(256) cache_combine_kernel(const int32_t *__res
     const float before = weight_in && j < nb ? weight_in[at] : 0.f;
     if (nt > 0) {
         for (int h = warp; h < G; h += 8) {
-            const float2 t = cache_join(ml, P.n, G, h, lane);
+            const float2 t = cache_join_partials(ml, P.n, G, h, lane, 32);
             if (lane == 0) head[h] = t;
         }
     }

@@ -994,9 +994,25 @@ ssa_status_t ssa_cache_decode(const ssa_dims_t *dims, const int32_t *cache_len, 
     const __nv_bfloat16 *qb = static_cast<const __nv_bfloat16 *>(q);
     CUtensorMap tmK, tmV;
     if (!make_tmap_codes(&tmK, K8, S.krows, S.s) || !make_tmap_codes(&tmV, V8, S.krows, S.s)) return SSA_ERR_CUDA;
-    if (S.k > 0)
-        cache_select_kernel<<<bhk, kTopThreads, static_cast<size_t>(S.nb) * 4, st>>>(cache_len, qb, Kbar, idx, S.Hk, S.G,
-                                                                                    S.T, S.s, S.k, S.nb);
+    if (S.k > 0) {
+        // CTAs per pair: a second one only from 128 blocks on (each scores 64 at a time), while SMs are idle
+        unsigned parts = 1;
+        while (parts < 8 && parts * 2 * bhk <= 2u * kCacheSms && static_cast<unsigned>(S.nb) >= 128 * parts) parts *= 2;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = parts;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(bhk * parts);
+        cfg.blockDim = dim3(kTopThreads);
+        cfg.dynamicSmemBytes = static_cast<size_t>(S.nb) * 4;
+        cfg.stream = st;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaLaunchKernelEx(&cfg, cache_select_kernel, cache_len, qb, Kbar, idx, S.Hk, S.G, S.T, S.s, S.k, S.nb) !=
+            cudaSuccess)
+            return SSA_ERR_CUDA;
+    }
     // no more CTAs than the caches can have tiles
     const size_t most = S.BHk * ((static_cast<size_t>(S.k > 0 ? S.k : S.nb) * S.s + 127) / 128);
     const unsigned grid = static_cast<unsigned>(most < cache_grid(S.G) ? most : cache_grid(S.G));
@@ -1022,13 +1038,15 @@ ssa_status_t ssa_cache_decode(const ssa_dims_t *dims, const int32_t *cache_len, 
                                : heads(std::integral_constant<int, 32>());
     if (!ok) return SSA_ERR_CUDA;
     // partials per pair: about grid / pairs, each of 128 values per head
-    const bool wide = grid / bhk >= 16;
-    const unsigned rows = static_cast<unsigned>(S.BH), head_ctas = wide ? rows : (rows + 7) / 8;
+    const unsigned split = grid < 16 * bhk ? 0 : grid < 64 * bhk ? 1 : 4;
+    auto combine = split == 0   ? cache_combine_kernel<0>
+                   : split == 1 ? cache_combine_kernel<1>
+                                : cache_combine_kernel<4>;
+    const unsigned rows = static_cast<unsigned>(S.BH), head_ctas = split ? split * rows : (rows + 7) / 8;
     const size_t weight_ctas = weight_out ? S.BHk * ((S.nb + 255) / 256) : 0;
-    if (!launch_dependent(wide ? cache_combine_kernel<8> : cache_combine_kernel<1>,
-                          dim3(static_cast<unsigned>(head_ctas + weight_ctas)), 256, 0, st, cache_len, opart, ml, block_ml,
-                          idx, static_cast<__nv_bfloat16 *>(o), lse, weight_in, weight_out, S.B, S.Hk, S.G, S.T, S.s, S.k,
-                          S.nb, static_cast<int>(grid), static_cast<int>(head_ctas)))
+    if (!launch_dependent(combine, dim3(static_cast<unsigned>(head_ctas + weight_ctas)), 256, 0, st, cache_len, opart, ml,
+                          block_ml, idx, static_cast<__nv_bfloat16 *>(o), lse, weight_in, weight_out, S.B, S.Hk, S.G, S.T,
+                          S.s, S.k, S.nb, static_cast<int>(grid), static_cast<int>(head_ctas)))
         return SSA_ERR_CUDA;
     return launch_status();
 }

@@ -133,11 +133,14 @@ __device__ __forceinline__ void top_ascending_warp(const uint32_t *keys, int n, 
 #pragma unroll 1
         for (; b > 0 && !exact; b -= 2) {
             const uint32_t c1 = tau + (1u << (b - 1)), c2 = tau + (2u << (b - 1)), c3 = tau + (3u << (b - 1));
-            uint32_t cnt = 0;
+            uint32_t k1 = 0, k2 = 0, k3 = 0;  // (chains of their own: one sum of all would be three times as long)
 #pragma unroll
-            for (int i = 0; i < KPL; ++i)
-                cnt += (key[i] >= c1 ? 1u : 0u) + (key[i] >= c2 ? 1u << 11 : 0u) + (key[i] >= c3 ? 1u << 22 : 0u);
-            cnt = __reduce_add_sync(0xffffffffu, cnt);
+            for (int i = 0; i < KPL; ++i) {
+                k1 += key[i] >= c1 ? 1u : 0u;
+                k2 += key[i] >= c2 ? 1u << 11 : 0u;
+                k3 += key[i] >= c3 ? 1u << 22 : 0u;
+            }
+            const uint32_t cnt = __reduce_add_sync(0xffffffffu, k1 + k2 + k3);
             const int n1 = cnt & 2047, n2 = (cnt >> 11) & 2047, n3 = cnt >> 22;
             int m = n;
             if (n3 >= kk)
