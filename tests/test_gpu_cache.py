@@ -76,13 +76,14 @@ def unchanged(c, before, where=slice(None)):
 def check_append(dims, c, before, lens, news, K, V):
     s, nb = dims.s, dims.T // dims.s
     Kbar = before[4].cpu().numpy()
-    for codes, scale, was, was_scale, X in ((c.K8, c.Kscale, before[0], before[1], K), (c.V8, c.Vscale, before[2], before[3], V)):
+    for keys, codes, scale, was, was_scale, X in ((True, c.K8, c.Kscale, before[0], before[1], K),
+                                                  (False, c.V8, c.Vscale, before[2], before[3], V)):
         want, want_scale = was.cpu().numpy().copy(), was_scale.double().cpu().numpy().copy()
         x = X.double().cpu().numpy()
         for b in range(dims.B):
             for h in range(dims.kv_heads):
                 done = R.append(x[b, h, :news[b]], want[b, h], want_scale[b, h], lens[b], s)
-                if X is K:
+                if keys:
                     for j in done:
                         rows = R.CODES[want[b, h, j * s:(j + 1) * s]] * want_scale[b, h, j]
                         got = c.Kbar[b, h, j].double().cpu().numpy()
@@ -545,3 +546,101 @@ def test_tensor_checks():
                  lambda: ops.cache_decode(L.make_dims(2, 4, 256, D, 64, 2, Hkv=2), c._replace(Kbar=None), lens, q)):
         with pytest.raises(L.SSAError):
             call()
+
+
+# ------------------------------------------------------------------------------- sizes, streams, capture
+def test_offsets_beyond_32_bits():
+    """A cache of 4.3 GB of codes each: the last sequence's rows lie beyond 2^32 bytes."""
+    B, Hk, s, T = 33, 8, 128, 131072
+    assert B * Hk * T * D > 2 ** 32
+    dims, sparse = L.make_dims(B, 16, T, D, s, 0, Hkv=Hk), L.make_dims(B, 16, T, D, s, 4, Hkv=Hk)
+    c = ops.Cache8.empty(dims)
+    last = L.make_dims(1, 16, T, D, s, 0, Hkv=Hk)
+    small = filled(last, [1500], seed=4)
+    for whole, one in zip(c, small):
+        whole.view(torch.uint8)[-1].copy_(one.view(torch.uint8)[0])
+    lens = torch.full((B,), -1, dtype=torch.int32, device="cuda")
+    lens[-1] = 1500
+    q = query(B, 16)
+    for dm in (dims, sparse):
+        w = torch.empty(B, Hk, T // s, device="cuda")
+        out = ops.cache_decode(dm, c, lens, q, weight_out=w)
+        one = [x[-1:] if x is not None else None for x in out]
+        check_decode(L.make_dims(1, 16, T, D, s, dm.k, Hkv=Hk), small, [1500], q[-1:], one, None, w[-1:])
+    # tokens into the last sequence, the same as into the small cache
+    K = torch.randn(B, Hk, 100, D, device="cuda", generator=gen(1)).bfloat16()
+    n_new = torch.zeros(B, dtype=torch.int32, device="cuda")
+    n_new[-1] = 100
+    ops.cache_append(dims, c, (lens + 1).contiguous(), K, -K, n_new)
+    ops.cache_append(last, small, i32(1501), K[-1:], -K[-1:])
+    weight = torch.rand(B, Hk, T // s, device="cuda", generator=gen(2))
+    held = (lens + 1 + n_new).contiguous()
+    kept, new_len = ops.cache_evict(dims, c, held, 7, weight)
+    kept1, new1 = ops.cache_evict(last, small, held[-1:].clone(), 7, weight[-1:].contiguous())
+    assert torch.equal(kept[-1:], kept1) and torch.equal(new_len[-1:], new1)
+    n = int(new1[0])
+    for whole, one in zip(c, small):
+        rows = n if whole.shape[2] == T else -(-n // s) if whole.dim() == 3 else n // s
+        assert torch.equal(whole[-1, :, :rows].contiguous().view(torch.uint8), one[0, :, :rows].contiguous().view(torch.uint8))
+    assert L.ssa_get_device_error() == L.SSA_OK
+
+
+def test_append_captured():
+    """A captured step of one token, replayed from inside a block across its end, and a captured piece."""
+    s, T = 64, 256
+    dims = L.make_dims(2, 2, T, D, s, 0)
+    for n, starts in ((1, (62, 63, 64)), (20, (50, 70, 108))):
+        lens = i32(0, 0)
+        c = filled(dims, [200, 200], garbage=False)
+        K = torch.empty(2, 2, n, D, dtype=torch.bfloat16, device="cuda")
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            ops.cache_append(dims, c, lens, K, K)
+        for i, at in enumerate(starts):
+            lens.copy_(torch.tensor([at, at + 17], dtype=torch.int32))
+            K.copy_(torch.randn(K.shape, device="cuda", generator=gen(i)) * 4.0 ** i)
+            before = snapshot(c)
+            g.replay()
+            torch.cuda.synchronize()
+            check_append(dims, c, before, [at, at + 17], [n, n], K, K)
+
+
+def test_two_calls_at_once():
+    """Decodes of two caches on two streams, each with its workspace, while the other runs."""
+    dims = [L.make_dims(8, 32, 4096, D, 128, 0, Hkv=8), L.make_dims(8, 16, 4096, D, 64, 9, Hkv=2)]
+    lens = [[4095 - 300 * i for i in range(8)], [100 + 500 * i for i in range(8)]]
+    caches = [filled(d, n, seed=i) for i, (d, n) in enumerate(zip(dims, lens))]
+    qs = [query(8, 32, 1), query(8, 16, 2)]
+    cl = [i32(*n) for n in lens]
+    ws = [ops._ws(d, L.SSA_OP_CACHE_DECODE, "cuda") for d in dims]
+    alone = [ops.cache_decode(d, c, n, q, ws=w) for d, c, n, q, w in zip(dims, caches, cl, qs, ws)]
+    torch.cuda.synchronize()
+    streams, outs = [torch.cuda.Stream(), torch.cuda.Stream()], [[], []]
+    for _ in range(10):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                outs[i].append(ops.cache_decode(dims[i], caches[i], cl[i], qs[i], ws=ws[i]))
+    torch.cuda.synchronize()
+    for want, got in zip(alone, outs):
+        for g in got:
+            assert all(torch.equal(a, b) for a, b in zip(want, g) if a is not None)
+    check_decode(dims[1], caches[1], lens[1], qs[1], alone[1])
+
+
+def test_decode_of_broadcast_and_strided_new_rows():
+    """Keys shared by every head (a stride of 0) are stored once per head; a batch of one with odd strides."""
+    dims = L.make_dims(1, 4, 256, D, 64, 0)
+    c, e = filled(dims, [9]), filled(dims, [9])
+    x = torch.randn(1, 1, 30, D, device="cuda", generator=gen(1)).bfloat16()
+    ops.cache_append(dims, c, i32(10), x.expand(1, 4, 30, D), x.expand(1, 4, 30, D))
+    y = x.expand(1, 4, 30, D).contiguous()
+    odd = torch.as_strided(y, y.shape, (7, 30 * D, D, 1))  # the stride of an extent of one is never used
+    ops.cache_append(dims, e, i32(10), odd, odd)
+    assert unchanged(c, snapshot(e))
+    short = torch.as_strided(y, y.shape, (4 * 30 * D, 30 * D, D, 1), 0)[..., 1:]  # off a 16-byte boundary
+    with pytest.raises((ValueError, L.SSAError)):
+        ops.cache_append(dims, c, i32(10), short, short)
+    wide = torch.zeros(1, 4, 30, 2 * D, dtype=torch.bfloat16, device="cuda")[..., ::2]
+    with pytest.raises(ValueError):
+        ops.cache_append(dims, c, i32(10), wide, wide)
