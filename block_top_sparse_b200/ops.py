@@ -174,13 +174,17 @@ class Cache8(NamedTuple):
         """ValueError unless the buffers are those of dims; returns the shape of the scales."""
         K8, Kscale, V8, Vscale, Kbar = self
         B, Hk, T, d = dims.B, dims.Hkv or dims.H, dims.T, dims.d
-        codes, scales = (B, Hk, T, d), (B, Hk, T // dims.s)
-        _is(K8, "K8", codes, torch.float8_e4m3fn, device)
-        _is(V8, "V8", codes, torch.float8_e4m3fn, device)
-        _is(Kscale, "Kscale", scales, torch.float32, device)
-        _is(Vscale, "Vscale", scales, torch.float32, device)
+        codes, scales = (B, Hk, T, d), (B, Hk, T // dims.s if dims.s > 0 else 0)
+        f8, f32 = torch.float8_e4m3fn, torch.float32
+        if not (K8.shape == codes and V8.shape == codes and Kscale.shape == scales and Vscale.shape == scales
+                and K8.dtype is f8 and V8.dtype is f8 and Kscale.dtype is f32 and Vscale.dtype is f32
+                and K8.get_device() == V8.get_device() == Kscale.get_device() == Vscale.get_device() == device
+                and K8.is_contiguous() and V8.is_contiguous() and Kscale.is_contiguous() and Vscale.is_contiguous()):
+            for t, name, shape, dtype in ((K8, "K8", codes, f8), (V8, "V8", codes, f8), (Kscale, "Kscale", scales, f32),
+                                          (Vscale, "Vscale", scales, f32)):
+                _is(t, name, shape, dtype, device)  # says which
         if Kbar is not None:
-            _is(Kbar, "Kbar", scales + (d,), torch.float32, device)
+            _is(Kbar, "Kbar", scales + (d,), f32, device)
         return scales
 
 
