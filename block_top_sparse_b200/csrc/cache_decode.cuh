@@ -262,7 +262,6 @@ __global__ void __launch_bounds__(128, CacheAttend<NH>::kPerSm) cache_attend_ker
     float2 *__restrict__ block_ml, int B, int Hk, int G, int T, int k, int nb, float scale_log2) {
     using SM = CacheAttend<NH>;
     constexpr int kPer = 128 / S;  // blocks of a tile
-    grid_dependents_launch();      // (takes effect once every CTA of this grid has started)
     extern __shared__ __align__(1024) uint8_t cad_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(cad_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -276,6 +275,15 @@ __global__ void __launch_bounds__(128, CacheAttend<NH>::kPerSm) cache_attend_ker
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 4);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + 5);
 
+    // Tensor memory first: the SM starts its next CTA only when this one has given up the right to allocate
+    // (measured: five CTAs per SM started 7.4 us apart with the allocation behind the search below, 38 us for
+    // 16 ragged sequences of up to 32K tokens).
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, SM::kTmemCols);
+        tmem_relinquish();
+    }
+    grid_dependents_launch();  // (takes effect once every CTA of this grid has started)
+
     // this CTA's share of the tiles
     const int64_t total = cache_total_tiles(cache_len, B, Hk, T, S, k, lane);
     if (blockIdx.x == 0)
@@ -285,6 +293,10 @@ __global__ void __launch_bounds__(128, CacheAttend<NH>::kPerSm) cache_attend_ker
         }
     const int64_t ctas = min(static_cast<int64_t>(gridDim.x), total);
     if (static_cast<int64_t>(blockIdx.x) >= ctas) {
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        if (warp == 1) tmem_dealloc(*tmem_slot, SM::kTmemCols);
         grid_dependency_wait();
         return;
     }
@@ -342,10 +354,6 @@ __global__ void __launch_bounds__(128, CacheAttend<NH>::kPerSm) cache_attend_ker
         for (int i = 0; i < 4; ++i) mbar_init(bars + i, 1);
         *abort_flag = 0;
         fence_barrier_init();
-    }
-    if (warp == 1) {
-        tmem_alloc(tmem_slot, SM::kTmemCols);
-        tmem_relinquish();
     }
     grid_dependency_wait();  // the selection (k > 0) has been written
     Blocks blk = blocks_of(cur), blk1 = blk, blk2 = blk;
