@@ -714,11 +714,12 @@ __global__ void __launch_bounds__(128, CacheAttend<NH>::kPerSm) cache_attend_ker
 
 // ---------------------------------------------------------------------------
 // Joining the partials: M = max m_i, l = sum 2^(m_i - M) l_i, o = sum 2^(m_i - M) o_i / l, in the order of the
-// CTAs.  The first head_ctas CTAs join query heads; every CTA after them adds up the attention weight of 256
-// blocks of one pair over its group's heads.  A head CTA takes eight heads, a warp each (SPLIT = 0), where there
-// are many pairs of few partials, one head (1), or a quarter of one head's dims (4) where a pair is split over
-// many CTAs: 16 sequences of up to 32K tokens, 2 key heads, about 23 partials a pair: 38 us in all with 1 and
-// 43 us with 4; one of 131072 tokens, 1 key head, 592 partials: 27 us and 18 us.
+// CTAs; the attention weight of the blocks from their own maxima and sums.  Where there are many pairs of few
+// partials a CTA takes eight heads of a pair, a warp each, then its share of the pair's blocks (SPLIT = 0).  Where a pair is
+// split over many CTAs, the first head_ctas CTAs take one head (SPLIT = 1) or a quarter of one head's dims (4)
+// each, and every CTA after them 256 blocks of one pair: 16 sequences of up to 32K tokens, 2 key heads, about
+// 23 partials a pair: 38 us in all with 1 and 43 us with 4; one of 131072 tokens, 1 key head, 592 partials: 27 us
+// and 18 us.
 // ---------------------------------------------------------------------------
 struct CachePartials {
     int n;
@@ -746,7 +747,7 @@ __device__ __forceinline__ void cache_join(float &m, float &l, float m2, float l
 // Maximum and sum over n partials of one head, by `threads` threads of which this is number t (a multiple of a
 // warp); the result is that of the thread's warp alone.
 __device__ __forceinline__ float2 cache_join_partials(const float2 *ml, int n, int G, int h, int t, int threads) {
-    constexpr int U = 8;
+    constexpr int U = 4;
     float m = -INFINITY, l = 0.f;
     for (int i0 = t; i0 < n; i0 += U * threads) {
         float2 a[U];
@@ -769,6 +770,20 @@ __device__ __forceinline__ float2 cache_join_partials(const float2 *ml, int n, i
     return make_float2(m, l);
 }
 
+// Adds partial i of a head, 16 bytes of its outputs.
+__device__ __forceinline__ void cache_add(float4 &a, float f, const float4 &v) {
+    a.x = fmaf(f, v.x, a.x), a.y = fmaf(f, v.y, a.y), a.z = fmaf(f, v.z, a.z), a.w = fmaf(f, v.w, a.w);
+}
+
+// Four outputs of one query head (t: its maximum and sum; tokens = false: o = 0, lse = -inf).
+__device__ __forceinline__ void cache_write(__nv_bfloat16 *o, float *lse, int row, int piece, const float4 &a,
+                                            const float2 &t, bool tokens) {
+    const float inv = tokens ? 1.f / t.y : 0.f;
+    reinterpret_cast<uint2 *>(o + static_cast<size_t>(row) * kCacheD)[piece] =
+        make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+    if (piece == 0) lse[row] = tokens ? fmaf(t.x, kLn2, logf(t.y)) : -INFINITY;
+}
+
 template <int SPLIT>
 __global__ void __launch_bounds__(256) cache_combine_kernel(const int32_t *__restrict__ cache_len,
                                                             const float *opart, const float2 *mlpart,
@@ -777,111 +792,102 @@ __global__ void __launch_bounds__(256) cache_combine_kernel(const int32_t *__res
                                                             const float *weight_in, float *weight_out, int B, int Hk,
                                                             int G, int T, int s, int k, int nb, int grid,
                                                             int head_ctas) {
+    constexpr int kSplit = SPLIT ? SPLIT : 1;
     __shared__ float2 head[kCacheMaxGroup];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const bool heads = static_cast<int>(blockIdx.x) < head_ctas;
+    const bool heads = SPLIT == 0 || static_cast<int>(blockIdx.x) < head_ctas;
     const int chunks = (nb + 255) / 256, w = blockIdx.x - head_ctas;
-    const int row = SPLIT ? blockIdx.x / max(SPLIT, 1) : blockIdx.x * 8 + warp;  // query head of the batch (head CTAs)
-    const int bh = heads ? min(row / G, B * Hk - 1) : w / chunks, b = bh / Hk;
+    const int parts = SPLIT == 0 ? (G + 7) / 8 : 1, part = SPLIT == 0 ? blockIdx.x % parts : 0;  // CTAs of a pair
+    const int bh = SPLIT == 0 ? blockIdx.x / parts : heads ? blockIdx.x / kSplit / G : w / chunks, b = bh / Hk;
     const int L = __ldg(cache_len + b), nt = cache_tiles(L, T, s, k), ns = cache_slots(L, T, s, k);
     const int64_t total = cache_total_tiles(cache_len, B, Hk, T, s, k, lane);
     const int64_t first = cache_tiles_before(cache_len, b, T, s, k, lane) * Hk + static_cast<int64_t>(bh % Hk) * nt;
     CachePartials P{0, 0};
     if (nt > 0) P = cache_partials_of(total, first, nt, grid, bh);
     const float2 *ml = mlpart + P.slot0 * G;
+    const size_t step = static_cast<size_t>(G) * (kCacheD / 4);
+    constexpr int U = 4;  // the first outputs are asked for along with the maxima
     grid_dependency_wait();
-    if (heads) {
-        const int h = row % G;
-        const bool mine = row < B * Hk * G;
-        const float4 *op = reinterpret_cast<const float4 *>(opart + (P.slot0 * G + h) * kCacheD);
-        const size_t step = static_cast<size_t>(G) * (kCacheD / 4);
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-        float2 t = make_float2(-INFINITY, 0.f);
-        auto add = [&](float f, const float4 &v) {
-            a.x = fmaf(f, v.x, a.x), a.y = fmaf(f, v.y, a.y), a.z = fmaf(f, v.z, a.z), a.w = fmaf(f, v.w, a.w);
-        };
-        int piece = lane;       // 16 bytes of fp32 outputs
-        bool write = mine;
-        if constexpr (SPLIT == 0) {
-            if (mine && nt > 0) {
-                constexpr int U = 4;  // the first outputs are asked for along with the maxima
-                float4 v0[U];
-                float m0[U];
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (u < P.n) {
-                        v0[u] = __ldcg(op + u * step + lane);
-                        m0[u] = __ldcg(ml + static_cast<size_t>(u) * G + h).x;
-                    }
-                t = cache_join_partials(ml, P.n, G, h, lane, 32);
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (u < P.n) add(fast_exp2(m0[u] - t.x), v0[u]);
-#pragma unroll 8
-                for (int i = U; i < P.n; ++i)
-                    add(fast_exp2(__ldcg(ml + static_cast<size_t>(i) * G + h).x - t.x), __ldcg(op + i * step + lane));
+    if constexpr (SPLIT == 0) {
+        for (int h = warp; weight_out && h < G; h += blockDim.x >> 5)  // the other CTAs' heads, for the weights
+            if (h / 8 != part) {
+                const float2 t = cache_join_partials(ml, P.n, G, h, lane, 32);
+                if (lane == 0) head[h] = t;
             }
-        } else {
-            constexpr int kLanes = 32 / SPLIT, kGroups = 256 / kLanes;  // groups of threads take partials in turn
-            __shared__ float2 part_ml[8];
-            __shared__ float4 part_o[8][kLanes];
-            const int group = tid / kLanes;
-            piece = blockIdx.x % SPLIT * kLanes + tid % kLanes;
-            write = mine && tid < kLanes;
-            if (nt > 0) {
-                constexpr int U = 4;
-                float4 v0[U];
-                float m0[U];
+        for (int h = 8 * part + warp; h < min(G, 8 * part + 8); h += blockDim.x >> 5) {
+            const float4 *op = reinterpret_cast<const float4 *>(opart + (P.slot0 * G + h) * kCacheD) + lane;
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f), v0[U];
+            float m0[U];
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int i = group + u * kGroups;
-                    if (i < P.n) {
-                        v0[u] = __ldcg(op + i * step + piece);
-                        m0[u] = __ldcg(ml + static_cast<size_t>(i) * G + h).x;
-                    }
+            for (int u = 0; u < U; ++u)
+                if (u < P.n) {
+                    v0[u] = __ldcg(op + u * step);
+                    m0[u] = __ldcg(ml + static_cast<size_t>(u) * G + h).x;
                 }
-                const float2 own = cache_join_partials(ml, P.n, G, h, tid, 256);
-                if (lane == 0) part_ml[warp] = own;
-                __syncthreads();
-                t = part_ml[0];
+            const float2 t = cache_join_partials(ml, P.n, G, h, lane, 32);
 #pragma unroll
-                for (int i = 1; i < 8; ++i) cache_join(t.x, t.y, part_ml[i].x, part_ml[i].y);
+            for (int u = 0; u < U; ++u)
+                if (u < P.n) cache_add(a, fast_exp2(m0[u] - t.x), v0[u]);
+#pragma unroll 4
+            for (int i = U; i < P.n; ++i)
+                cache_add(a, fast_exp2(__ldcg(ml + static_cast<size_t>(i) * G + h).x - t.x), __ldcg(op + i * step));
+            cache_write(o, lse, bh * G + h, lane, a, t, nt > 0);
+            if (lane == 0) head[h] = t;
+        }
+    } else if (heads) {
+        constexpr int kLanes = 32 / kSplit, kGroups = 256 / kLanes;  // take partials in turn
+        __shared__ float2 part_ml[8];
+        __shared__ float4 part_o[8][kLanes];
+        const int row = blockIdx.x / kSplit, h = row % G, group = tid / kLanes;
+        const int piece = blockIdx.x % kSplit * kLanes + tid % kLanes;
+        const float4 *op = reinterpret_cast<const float4 *>(opart + (P.slot0 * G + h) * kCacheD) + piece;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f), v0[U];
+        float m0[U];
 #pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (group + u * kGroups < P.n) add(fast_exp2(m0[u] - t.x), v0[u]);
-#pragma unroll 8
-                for (int i = group + U * kGroups; i < P.n; i += kGroups)
-                    add(fast_exp2(__ldcg(ml + static_cast<size_t>(i) * G + h).x - t.x), __ldcg(op + i * step + piece));
-#pragma unroll
-                for (int off = kLanes; off < 32; off <<= 1) {
-                    a.x += __shfl_xor_sync(0xffffffffu, a.x, off), a.y += __shfl_xor_sync(0xffffffffu, a.y, off);
-                    a.z += __shfl_xor_sync(0xffffffffu, a.z, off), a.w += __shfl_xor_sync(0xffffffffu, a.w, off);
-                }
-                if (lane < kLanes) part_o[warp][lane] = a;
-                __syncthreads();
-                if (tid < kLanes)
-#pragma unroll
-                    for (int i = 1; i < 8; ++i) add(1.f, part_o[i][tid]);
+        for (int u = 0; u < U; ++u) {
+            const int i = group + u * kGroups;
+            if (i < P.n) {
+                v0[u] = __ldcg(op + i * step);
+                m0[u] = __ldcg(ml + static_cast<size_t>(i) * G + h).x;
             }
         }
-        if (write) {
-            const float inv = nt > 0 ? 1.f / t.y : 0.f;  // no token (or a bad length): o = 0
-            reinterpret_cast<uint2 *>(o + static_cast<size_t>(row) * kCacheD)[piece] =
-                make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
-            if (piece == 0) lse[row] = nt > 0 ? fmaf(t.x, kLn2, logf(t.y)) : -INFINITY;
+        const float2 own = cache_join_partials(ml, P.n, G, h, tid, 256);
+        if (lane == 0) part_ml[warp] = own;
+        __syncthreads();
+        float2 t = part_ml[0];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) cache_join(t.x, t.y, part_ml[i].x, part_ml[i].y);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (group + u * kGroups < P.n) cache_add(a, fast_exp2(m0[u] - t.x), v0[u]);
+#pragma unroll 8
+        for (int i = group + U * kGroups; i < P.n; i += kGroups)
+            cache_add(a, fast_exp2(__ldcg(ml + static_cast<size_t>(i) * G + h).x - t.x), __ldcg(op + i * step));
+#pragma unroll
+        for (int off = kLanes; off < 32; off <<= 1) {
+            a.x += __shfl_xor_sync(0xffffffffu, a.x, off), a.y += __shfl_xor_sync(0xffffffffu, a.y, off);
+            a.z += __shfl_xor_sync(0xffffffffu, a.z, off), a.w += __shfl_xor_sync(0xffffffffu, a.w, off);
+        }
+        if (lane < kLanes) part_o[warp][lane] = a;
+        __syncthreads();
+        if (tid < kLanes) {
+#pragma unroll
+            for (int i = 1; i < 8; ++i) cache_add(a, 1.f, part_o[i][tid]);
+            cache_write(o, lse, row, piece, a, t, nt > 0);
         }
         return;
-    }
-    // attention weight of blocks [j0, j0 + 256)
-    const int j0 = w % chunks * 256, j = j0 + tid;
-    const size_t at = static_cast<size_t>(bh) * nb + j;
-    const float before = weight_in && j < nb ? weight_in[at] : 0.f;
-    if (nt > 0) {
+    } else if (nt > 0) {
         for (int h = warp; h < G; h += 8) {
             const float2 t = cache_join_partials(ml, P.n, G, h, lane, 32);
             if (lane == 0) head[h] = t;
         }
     }
+    if (!weight_out) return;
+    // attention weight of blocks [j0, j1)
+    const int share = SPLIT == 0 ? (nb + parts - 1) / parts : 256;
+    const int j0 = SPLIT == 0 ? part * share : w % chunks * 256, j1 = min(j0 + share, nb);
+    const float *win = weight_in ? weight_in + static_cast<size_t>(bh) * nb : nullptr;
+    float *wout = weight_out + static_cast<size_t>(bh) * nb;
     auto mass = [&](int slot, int slots) {  // of one attended block
         float sum = 0.f;
         const float2 *bl = block_ml + static_cast<size_t>(bh) * G * slots + slot;
@@ -894,13 +900,15 @@ __global__ void __launch_bounds__(256) cache_combine_kernel(const int32_t *__res
     };
     if (k == 0) {
         __syncthreads();
-        if (j < nb) weight_out[at] = before + (j < ns ? mass(j, nb) : 0.f);
+        for (int j = j0 + tid; j < j1; j += blockDim.x) wout[j] = (win ? win[j] : 0.f) + (j < ns ? mass(j, nb) : 0.f);
     } else {
-        if (j < nb) weight_out[at] = before;
+        // every block first, then the attended ones, which are distinct (weight_in may be weight_out: the first
+        // writes leave its values)
+        for (int j = j0 + tid; j < j1; j += blockDim.x) wout[j] = win ? win[j] : 0.f;
         __syncthreads();
-        for (int i = tid; i < ns; i += 256) {  // attended blocks are distinct
-            const int jj = __ldcg(idx + static_cast<size_t>(bh) * k + i);
-            if (jj >= j0 && jj < min(j0 + 256, nb)) weight_out[static_cast<size_t>(bh) * nb + jj] += mass(i, k);
+        for (int i = tid; i < ns; i += blockDim.x) {
+            const int j = __ldcg(idx + static_cast<size_t>(bh) * k + i);
+            if (j >= j0 && j < j1) wout[j] = (win ? win[j] : 0.f) + mass(i, k);
         }
     }
 }

@@ -1042,11 +1042,13 @@ ssa_status_t ssa_cache_decode(const ssa_dims_t *dims, const int32_t *cache_len, 
     auto combine = split == 0   ? cache_combine_kernel<0>
                    : split == 1 ? cache_combine_kernel<1>
                                 : cache_combine_kernel<4>;
-    const unsigned rows = static_cast<unsigned>(S.BH), head_ctas = split ? split * rows : (rows + 7) / 8;
-    const size_t weight_ctas = weight_out ? S.BHk * ((S.nb + 255) / 256) : 0;
-    if (!launch_dependent(combine, dim3(static_cast<unsigned>(head_ctas + weight_ctas)), 256, 0, st, cache_len, opart, ml,
-                          block_ml, idx, static_cast<__nv_bfloat16 *>(o), lse, weight_in, weight_out, S.B, S.Hk, S.G, S.T,
-                          S.s, S.k, S.nb, static_cast<int>(grid), static_cast<int>(head_ctas)))
+    const unsigned head_ctas = split ? split * static_cast<unsigned>(S.BH) : bhk * ((S.G + 7) / 8);
+    const size_t weight_ctas = split && weight_out ? S.BHk * ((S.nb + 255) / 256) : 0;
+    // (four warps are enough for up to four heads, and more of the small CTAs start beside the attention's)
+    if (!launch_dependent(combine, dim3(static_cast<unsigned>(head_ctas + weight_ctas)), split == 0 && S.G <= 4 ? 128 : 256,
+                          0, st, cache_len, opart, ml, block_ml, idx, static_cast<__nv_bfloat16 *>(o), lse, weight_in,
+                          weight_out, S.B, S.Hk, S.G, S.T, S.s, S.k, S.nb, static_cast<int>(grid),
+                          static_cast<int>(head_ctas)))
         return SSA_ERR_CUDA;
     return launch_status();
 }
