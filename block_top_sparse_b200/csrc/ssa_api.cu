@@ -965,7 +965,7 @@ ssa_status_t ssa_cache_append(const ssa_dims_t *dims, int n, const int32_t *cach
     if (blocks > S.nb) blocks = S.nb;
     const dim3 grid(static_cast<unsigned>(S.BHk), blocks, 2);
     auto kernel = S.s == 128 ? cache_append_kernel<128> : cache_append_kernel<64>;
-    kernel<<<grid, 2 * S.s, 0, cst>>>(
+    kernel<<<grid, append_threads(S.s), 0, cst>>>(
         cache_len, n_new, n, X[0], X[1], static_cast<uint8_t *>(K8), Kscale, static_cast<uint8_t *>(V8), Vscale, Kbar,
         S.Hk, S.T);
     return launch_status();
