@@ -65,7 +65,7 @@ constexpr int kAppendPasses = 8;
 constexpr int append_threads(int s) { return 16 * s / kAppendPasses; }
 
 template <int S>
-__global__ void __launch_bounds__(append_threads(S)) cache_append_kernel(
+__global__ void __launch_bounds__(append_threads(S), 1024 / append_threads(S)) cache_append_kernel(
     const int32_t *__restrict__ cache_len, const int32_t *__restrict__ n_new, int n, const CacheRows K,
     const CacheRows V, uint8_t *K8, float *Kscale, uint8_t *V8, float *Vscale, float *Kbar, int Hk, int T) {
     constexpr int P = kAppendPasses, kRows = S / P, kThreads = append_threads(S), kWarps = kThreads / 32;
@@ -116,34 +116,40 @@ __global__ void __launch_bounds__(append_threads(S)) cache_append_kernel(
     };
     uint32_t top = block_max(max(top2 & 0xFFFFu, top2 >> 16));
     const bool special = top >= 0x7F80u;  // (uniform) an infinity or a NaN among the new rows
-    if (special) {  // the scale goes by the finite elements
+    if (special) {  // the scale goes by the finite elements; infinities become NaN
         uint32_t m = 0;
 #pragma unroll
         for (int p = 0; p < P; ++p) {
-            const uint32_t w[4] = {v[p].x, v[p].y, v[p].z, v[p].w};
+            uint32_t w[4] = {v[p].x, v[p].y, v[p].z, v[p].w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const uint32_t lo = w[i] & 0x7FFFu, hi = (w[i] >> 16) & 0x7FFFu;
-                if (lo < 0x7F80u) m = max(m, lo);
-                if (hi < 0x7F80u) m = max(m, hi);
+                if (lo < 0x7F80u)
+                    m = max(m, lo);
+                else
+                    w[i] |= 0x7FFFu;
+                if (hi < 0x7F80u)
+                    m = max(m, hi);
+                else
+                    w[i] |= 0x7FFF0000u;
             }
+            v[p] = make_uint4(w[0], w[1], w[2], w[3]);
         }
         top = block_max(m);
     }
     const float want = fmaxf(e4m3_scale(__uint_as_float(top << 16)), old);
     const float inv = pow2_inverse(want);
     const bool pool = keys && Kbar && r1 == S;  // the block is complete: its mean key (uniform)
-    float sum[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) sum[i] = 0.f;
+    uint64_t sum[4] = {0, 0, 0, 0};  // of this thread's eight columns, in pairs
     auto add = [&](const uint2 &w) {
         const uint32_t q[2] = {w.x, w.y};
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const float2 a = unpack_e4m3x2(static_cast<uint16_t>(q[i])), c = unpack_e4m3x2(static_cast<uint16_t>(q[i] >> 16));
-            sum[4 * i] += a.x, sum[4 * i + 1] += a.y, sum[4 * i + 2] += c.x, sum[4 * i + 3] += c.y;
+            sum[2 * i] = fadd2(sum[2 * i], unpack_e4m3x2_f2(static_cast<uint16_t>(q[i])));
+            sum[2 * i + 1] = fadd2(sum[2 * i + 1], unpack_e4m3x2_f2(static_cast<uint16_t>(q[i] >> 16)));
         }
     };
+    const uint64_t inv2 = f2_pack(inv, inv);
     if (r0 > 0 && (want > old || pool)) {  // older rows: moved to a larger scale, or summed
         const float ratio = old * inv;
         for (int r = rr; r < r0; r += kRows) {
@@ -172,8 +178,8 @@ __global__ void __launch_bounds__(append_threads(S)) cache_append_kernel(
         uint32_t c[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            float lo = __uint_as_float(w[i] << 16) * inv, hi = __uint_as_float(w[i] & 0xFFFF0000u) * inv;
-            if (special) lo = (lo - lo) + lo, hi = (hi - hi) + hi;  // infinity -> NaN
+            float lo, hi;
+            f2_unpack(fmul2(f2_pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u)), inv2), lo, hi);
             c[i] = pack_e4m3x2(lo, hi);
         }
         const uint2 q = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
@@ -183,7 +189,7 @@ __global__ void __launch_bounds__(append_threads(S)) cache_append_kernel(
     if (threadIdx.x == 0) *scale = want;
     if (pool) {  // sums of codes are multiples of 2^-9 and mostly exact in fp32
 #pragma unroll
-        for (int i = 0; i < 8; ++i) col[rr][u * 8 + i] = sum[i];
+        for (int i = 0; i < 4; ++i) f2_unpack(sum[i], col[rr][u * 8 + 2 * i], col[rr][u * 8 + 2 * i + 1]);
         __syncthreads();
         for (int c = threadIdx.x; c < kCacheD; c += kThreads) {
             float a = 0.f;
