@@ -29,7 +29,7 @@
 //                          sum for each pair that it touches;
 //   cache_combine_kernel   joins a pair's partials in a fixed order; block weights
 //                          from the blocks' own maxima and sums.
-// No atomics: results are the same from run to run.
+// Atomics only where their order does not matter (maxima, counts): results are the same from run to run.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -102,7 +102,10 @@ __global__ void __launch_bounds__(kTopThreads, 4) cache_select_kernel(const int3
     if (want == bt) {
         for (int i = tid; i < want; i += kTopThreads) out[i] = i;
     } else if (want > 0) {
-        __syncthreads();
+        if (parts > 1)
+            cg::this_cluster().sync();  // the first CTA runs: its shared memory may be written
+        else
+            __syncthreads();
         double q4[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) q4[i] = qs[4 * lane + i];
@@ -252,8 +255,8 @@ struct CacheAttend {
 // memory.  A tile is a chain of dependent steps (product, maximum, weights, product, output), so the CTA is
 // kept small -- one tile of keys and one of values, each loaded again as soon as its product has read it --
 // and up to five CTAs per SM run their chains beside one another's loads: 160 KB in flight or in use per SM.
-// (Two tiles of each and three CTAs per SM: 786 us instead of 498 us for 64 caches of 16K to 32K tokens, 8 key
-// heads, G = 4.)
+// (Two tiles of each and three CTAs per SM: 784 us instead of 481 us for 64 caches of 16K to 32K tokens, 8 key
+// heads, G = 4; 472 us, 6.8 TB/s, with the steps since.)
 template <int NH, int S>
 __global__ void __launch_bounds__(128, CacheAttend<NH>::kPerSm) cache_attend_kernel(
     const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
@@ -276,8 +279,8 @@ __global__ void __launch_bounds__(128, CacheAttend<NH>::kPerSm) cache_attend_ker
     volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + 5);
 
     // Tensor memory first: the SM starts its next CTA only when this one has given up the right to allocate
-    // (measured: five CTAs per SM started 7.4 us apart with the allocation behind the search below, 38 us for
-    // 16 ragged sequences of up to 32K tokens).
+    // (measured: with the allocation behind the search below the fifth CTA of an SM started 7.4 us after the first,
+    // now 2.2 us; 16 ragged sequences of up to 32K tokens 38 -> 36 us in all).
     if (warp == 1) {
         tmem_alloc(tmem_slot, SM::kTmemCols);
         tmem_relinquish();

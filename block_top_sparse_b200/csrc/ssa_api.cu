@@ -294,7 +294,9 @@ bool launch_dependent(void (*kernel)(P...), dim3 grid, unsigned threads, size_t 
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...) == cudaSuccess;
+    if (cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...) == cudaSuccess) return true;
+    cudaGetLastError();  // reported by this call, not by the next one
+    return false;
 }
 
 // e4m3 rows of 128 bytes, boxes of one block.
@@ -888,10 +890,22 @@ ssa_status_t ssa_rope_axes(const ssa_dims_t *dims, const int32_t *pos, int axes,
             if (extent[i] == 1) X.is[i] = X.os[i] = 0;
         }
         if (!in) return true;
+        int order[3] = {0, 1, 2};
         for (int i = 0; i < 3; ++i) {
             if (X.is[i] < 0 || X.is[i] * esz % 16 || X.os[i] * esz % 16) return false;
-            if (extent[i] > 1 && X.os[i] < d) return false;
             if (in == out && X.is[i] != X.os[i]) return false;
+            for (int j = i; j > 0 && X.os[order[j]] < X.os[order[j - 1]]; --j) {
+                const int a = order[j];
+                order[j] = order[j - 1];
+                order[j - 1] = a;
+            }
+        }
+        int64_t span = d;  // elements that the dimensions of smaller strides cover
+        for (int i = 0; i < 3; ++i) {
+            const int a = order[i];
+            if (extent[a] == 1) continue;
+            if (X.os[a] < span) return false;
+            span += X.os[a] * (extent[a] - 1);
         }
         return ((reinterpret_cast<uintptr_t>(in) | reinterpret_cast<uintptr_t>(out)) & 15u) == 0;
     };
@@ -1010,8 +1024,10 @@ ssa_status_t ssa_cache_decode(const ssa_dims_t *dims, const int32_t *cache_len, 
         cfg.attrs = attr;
         cfg.numAttrs = 1;
         if (cudaLaunchKernelEx(&cfg, cache_select_kernel, cache_len, qb, Kbar, idx, S.Hk, S.G, S.T, S.s, S.k, S.nb) !=
-            cudaSuccess)
+            cudaSuccess) {
+            cudaGetLastError();
             return SSA_ERR_CUDA;
+        }
     }
     // no more CTAs than the caches can have tiles
     const size_t most = S.BHk * ((static_cast<size_t>(S.k > 0 ? S.k : S.nb) * S.s + 127) / 128);

@@ -223,6 +223,8 @@ def cache_decode(dims: L.Dims, cache: Cache8, cache_len: torch.Tensor, q: torch.
     idx = cache_len.new_empty((dims.B, dims.kv_heads, dims.k)) if dims.k > 0 else None
     if ws is None:
         ws = _ws(dims, L.SSA_OP_CACHE_DECODE, q.device)
+    elif ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError("ws must be contiguous on cuda:%d" % dev)
     L.ssa_cache_decode(dims, cache_len, q, cache.K8, cache.Kscale, cache.V8, cache.Vscale, cache.Kbar, idx, o, lse,
                        weight_in, weight_out, ws)
     return o, lse, idx
@@ -247,6 +249,8 @@ def cache_evict(dims: L.Dims, cache: Cache8, cache_len: torch.Tensor, keep: int,
     kept = cache_len.new_empty((dims.B, dims.kv_heads, max(int(keep), 0)))
     if ws is None:
         ws = _ws(dims, L.SSA_OP_CACHE_EVICT, weight.device)
+    elif ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError("ws must be contiguous on cuda:%d" % dev)
     L.ssa_cache_evict(dims, keep, cache_len, weight, cache.K8, cache.Kscale, cache.V8, cache.Vscale, kept, cache.Kbar,
                       weight_out, new_len, sink, recent, ws)
     return kept, new_len

@@ -366,8 +366,9 @@ ssa_status_t ssa_rope(const ssa_dims_t *dims, void *X, int heads, int pos0, floa
  *   *_strides  host arrays of 3: elements from one sequence, head, token to the
  *              next (a row's d elements are adjacent); NULL: contiguous.  Rows
  *              of a projection ([B, T, heads, d]) need no copy.  Strides are
- *              multiples of 16 bytes and >= 0, those of outputs >= d and such
- *              that no two rows overlap; base addresses are 16-byte aligned.
+ *              multiples of 16 bytes and >= 0; those of outputs nest (each is
+ *              at least what the dimensions of smaller strides cover), so that no
+ *              two rows overlap; base addresses are 16-byte aligned.
  */
 ssa_status_t ssa_rope_axes(const ssa_dims_t *dims, const int32_t *pos, int axes, const int32_t *sections,
                            unsigned flags, float base, float factor, const void *Q, const int64_t *q_strides, void *Qr,
@@ -395,7 +396,7 @@ ssa_status_t ssa_rope_axes(const ssa_dims_t *dims, const int32_t *pos, int axes,
  * ssa_cache_append writes n_new[b] tokens of sequence b (NULL: n for all; 0
  * allowed) at positions cache_len[b] ..
  *   K, V       in  [B, Hkv, n, d] bf16, n >= 1; strides as for ssa_rope_axes
- *              (NULL: contiguous); rows from n_new[b] on are not read
+ *              (NULL: contiguous); what rows from n_new[b] on hold does not matter
  *   n_new      in  [B] int32 or NULL
  *   K8, Kscale, V8, Vscale  in/out.  The scale of a touched block is the smallest
  *              2^p >= 2^-126 with max |x| / 2^p <= 448 over the call's finite

@@ -139,6 +139,10 @@ def test_rope_axes_refusals():
     assert call(d, qs=st(5120, 640, -128)) == INV
     assert call(d, qrs=st(5120, 640, 0)) == INV        # output rows on top of one another
     assert call(d, qs=st(5120, 128, 1024)) == INV      # in place with other strides
+    far = ctypes.c_void_p(1 << 20)
+    assert call(d, Qr=far, qrs=st(5120, 128, 128)) == INV       # rows of two heads on top of each other
+    assert call(d, Qr=far, qrs=st(5120 - 128, 640, 128)) == INV  # the last row of a sequence and the next one's first
+    assert call(d, Qr=far, qrs=st(640, 128, 1024)) == INV
 
 
 def test_plain_forms():

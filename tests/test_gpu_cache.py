@@ -542,7 +542,11 @@ def test_tensor_checks():
     for call in bad:
         with pytest.raises(ValueError):
             call()
-    for call in (lambda: ops.cache_evict(dims, c, lens, 0, w), lambda: ops.cache_evict(dims, c, lens, 2, w, sink=3),
+    ws = torch.empty(L.ssa_workspace_size(dims, L.SSA_OP_CACHE_DECODE), dtype=torch.uint8)
+    for call in (lambda: ops.cache_decode(dims, c, lens, q, ws=ws), lambda: ops.cache_evict(dims, c, lens, 2, w, ws=ws)):
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: ops.cache_decode(dims, c, lens, q, ws=ws[:-1].cuda()), lambda: ops.cache_evict(dims, c, lens, 0, w), lambda: ops.cache_evict(dims, c, lens, 2, w, sink=3),
                  lambda: ops.cache_decode(L.make_dims(2, 4, 256, D, 64, 2, Hkv=2), c._replace(Kbar=None), lens, q)):
         with pytest.raises(L.SSAError):
             call()
