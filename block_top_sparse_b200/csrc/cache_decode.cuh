@@ -13,8 +13,10 @@
 // as they are (tcgen05 kind::f8f6f4, nothing is converted or copied), and the
 // other operand is brought to e4m3 without losing its precision, as a sum of
 // terms of 4 significant bits each:
-//   q = 2^e (t0 + t1/16):          8 significant bits (bf16) in two terms,
-//   p = (t0 + t1/16 + t2/256)/256: 12 bits, error <= 2^-13 p + 2^-26.
+//   q = 2^e (t0 + t1/16):          8 significant bits (bf16) in two terms, or 2^-22 of the
+//                                  head's largest element,
+//   p = (t0 + t1/16 + t2/256)/256: 12 bits, error <= 2^-12 p (three roundings, each at
+//                                  most 2^-4 of what is left) + 2^-26 of a tile's largest.
 // The terms are extra columns (N) of the same product, and its results are put
 // together in fp32; N is small and the tensor cores have time to spare.
 //
@@ -233,8 +235,8 @@ struct CacheAttend {
     static constexpr int kQ = 2 * kTile;                             // [kNS][128 B]
     static constexpr int kP = kQ + kNS * 128;                        // [kNP / 16][128 keys][16 B]
     static constexpr int kRed = kP + kNP * 128;                      // two of: [NH][4 warps] sums
-    static constexpr int kHead = kRed + 2 * NH * 16;                 // [NH] logit factor, [2][NH] maximum, [NH] sum
-    static constexpr int kBar = kHead + 4 * NH * 4;
+    static constexpr int kHead = kRed + 2 * NH * 16;                 // [3][NH] factors, [3][2][NH] maxima
+    static constexpr int kBar = kHead + 9 * NH * 4;
     static constexpr int kBytes = kBar + 64 + 1024;                  // + alignment of the dynamic base to 1024 B
     // the logits' columns may be written again while the outputs are read, except at NH = 32, where both
     // products would take 256 columns a CTA and the outputs take the logits' place
@@ -249,10 +251,12 @@ struct CacheAttend {
 
 // Tile of 128 keys (one block of 128 or two of 64):
 //   S^T [128 keys x 2 NH] = K8 . (q terms)^T      A: keys as loaded (K-major), thread = key
-//   weights of the thread's key against the running maxima, split into three terms
+//   weights of the thread's key against the tile's maxima, split into three terms
 //   O^T [128 dims x 3 NH] = V8^T . (p terms)^T    A: values as loaded (M-major), thread = dim
-// The outputs stay in registers, brought to the new maximum tile by tile; only O^T of one tile is in tensor
-// memory.  A tile is a chain of dependent steps (product, maximum, weights, product, output), so the CTA is
+// A tile's weights are relative to its own maximum, so their 2^-26 is of the tile's largest weight, however much
+// larger another tile's is; where the values of two blocks of 64 in a tile have scales more than 2^6 apart, it is
+// of the largest product of weight and scale.  The outputs stay in registers, brought to the running maximum tile
+// by tile; only O^T of one tile is in tensor memory.  A tile is a chain of dependent steps (product, maximum, weights, product, output), so the CTA is
 // kept small -- one tile of keys and one of values, each loaded again as soon as its product has read it --
 // and up to five CTAs per SM run their chains beside one another's loads: 160 KB in flight or in use per SM.
 // (Two tiles of each and three CTAs per SM: 784 us instead of 481 us for 64 caches of 16K to 32K tokens, 8 key
@@ -269,9 +273,12 @@ __global__ void __launch_bounds__(128, CacheAttend<NH>::kPerSm) cache_attend_ker
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(cad_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t sK = smem_u32(smem), sV = sK + SM::kTile, sQ = sK + SM::kQ, sP = sK + SM::kP;
-    float *head_f = reinterpret_cast<float *>(smem + SM::kHead), *head_m = head_f + NH, *head_l = head_m + 2 * NH;
-    // running maximum of a head before any key: below every finite logit, so that a masked or overflowing one
-    // (-inf) weighs 0
+    // per head: logit factor; what a tile multiplies the outputs so far by, and its own
+    float *head_f = reinterpret_cast<float *>(smem + SM::kHead), *head_old = head_f + NH, *head_new = head_f + 2 * NH;
+    // maxima of a tile per block and head, raised by the warps; three in turn, the one after the next being reset
+    // while others may already raise the next
+    float *tile_m = head_f + 3 * NH;
+    // maximum of no key: below every finite logit, so that a masked or overflowing one (-inf) weighs 0
     constexpr float kLowest = -3.4e38f;
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + SM::kBar);
     uint64_t *bar_k = bars, *bar_v = bars + 1, *bar_s = bars + 2, *bar_o = bars + 3;
@@ -337,17 +344,16 @@ __global__ void __launch_bounds__(128, CacheAttend<NH>::kPerSm) cache_attend_ker
                 tma_load_2d(map, bar, smem + off + i * S * kCacheD, 0, (p.b * Hk + p.hk) * T + r.v[i] * S);
     };
     struct Scales {
-        float k, v, top;  // this key's block's; the largest value scale of the tile
+        float k, v[2];  // of this key's block; of the tile's blocks (0: none)
     };
     auto scales_of = [&](const TilePos &p, const Blocks &r) {
         const size_t at = (static_cast<size_t>(p.b) * Hk + p.hk) * nb;
-        Scales c{0.f, 0.f, 0.f};
+        Scales c{0.f, {0.f, 0.f}};
 #pragma unroll
         for (int i = 0; i < kPer; ++i)
             if (r.v[i] >= 0) {
-                const float v = __ldg(Vscale + at + r.v[i]);
-                c.top = fmaxf(c.top, v);
-                if (i == tid / S) c.v = v, c.k = __ldg(Kscale + at + r.v[i]);
+                c.v[i] = __ldg(Vscale + at + r.v[i]);
+                if (i == tid / S) c.k = __ldg(Kscale + at + r.v[i]);
             }
         return c;
     };
@@ -369,7 +375,8 @@ __global__ void __launch_bounds__(128, CacheAttend<NH>::kPerSm) cache_attend_ker
     // rows of heads past G stay zero: logits 0, nothing of them is written
     for (int e = tid; e < SM::kNS * 8; e += 128)
         *reinterpret_cast<uint4 *>(smem + SM::kQ + e * 16) = make_uint4(0u, 0u, 0u, 0u);
-    if (tid < NH) head_f[tid] = 0.f, head_m[tid] = head_m[NH + tid] = kLowest, head_l[tid] = 0.f;
+    if (tid < NH) head_f[tid] = 0.f;
+    for (int e = tid; e < 6 * NH; e += 128) tile_m[e] = kLowest;
     Scales sc = scales_of(cur, blk), sc1 = sc;
     TilePos pos1 = cur, pos2;
     if (n_tiles > 1) {
@@ -416,7 +423,9 @@ __global__ void __launch_bounds__(128, CacheAttend<NH>::kPerSm) cache_attend_ker
     if (NH <= 16) load_q(cur.b * Hk + cur.hk);
 
     uint64_t o[NH / 2];  // outputs of heads 2 i and 2 i + 1, this thread's dim
-    int pair = -1;
+    float m_run = kLowest, l_run = 0.f;  // (threads below NH) the head's maximum and sum
+    int pair = -1, turn = 0;
+    bool failed = false;
     for (int it = 0; it < n_tiles; ++it) {
         const uint32_t ph = it & 1;
         const int bh = cur.b * Hk + cur.hk;
@@ -459,12 +468,11 @@ __global__ void __launch_bounds__(128, CacheAttend<NH>::kPerSm) cache_attend_ker
                 if (lane == 0) {
                     // an infinity or NaN in the query makes the row's results NaN, not large
                     head_f[h] = finite ? unit * scale_log2 : __int_as_float(0x7FC00000);
-                    head_m[h] = head_m[NH + h] = kLowest;
-                    head_l[h] = 0.f;
                 }
             }
 #pragma unroll
             for (int i = 0; i < NH / 2; ++i) o[i] = 0;
+            m_run = kLowest, l_run = 0.f;
             fence_proxy_async_smem();
             __syncthreads();
         }
@@ -483,9 +491,7 @@ __global__ void __launch_bounds__(128, CacheAttend<NH>::kPerSm) cache_attend_ker
         const int my_blk = kPer == 1 ? blk.v[0] : (tid < S ? blk.v[0] : blk.v[kPer - 1]);
         const bool valid = my_blk >= 0 && my_blk * S + tid % S <= cur.L;
         float *red_l = reinterpret_cast<float *>(smem + SM::kRed + (it & 1) * NH * 16);
-        // Maxima before (old) and with (now) this tile.  They change places tile by tile, so that warps may raise
-        // those of the next tile while others still read these.
-        float *now_m = head_m + (it & 1 ? 0 : NH), *old_m = head_m + (it & 1 ? NH : 0);
+        float *now_m = tile_m + turn * 2 * NH;  // block, head
         uint64_t p[NH / 2];  // logits, then weights, of heads 2 i and 2 i + 1
         {
             const uint32_t row = tmem + (static_cast<uint32_t>(warp * 32) << 16);
@@ -525,39 +531,58 @@ __global__ void __launch_bounds__(128, CacheAttend<NH>::kPerSm) cache_attend_ker
                 asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(mc) : "f"(c));
                 mine = lane == 2 * i ? ma : lane == 2 * i + 1 ? mc : mine;
             }
-            if (lane < NH) atomic_max_shared(now_m + lane, mine);
+            if (lane < NH) atomic_max_shared(now_m + tid / S * NH + lane, mine);
         }
         tc_fence_before();
         __syncthreads();
-        // weights against the new maximum, in units of 1/256 of the tile's largest value scale
+        // weights against the tile's maximum; for the product with the values in units of 1/256 of the tile's
+        // largest value scale, or (wide) of its largest product of weight and scale
         float sum[NH];
-        bool grown = false;
-        const float head_old = tid < NH ? old_m[tid] : 0.f;  // (behind the next barrier others raise it)
-        const float unit = kPer == 1 ? 256.f : (sc.top > 0.f ? 256.f * (sc.v / sc.top) : 0.f);  // powers of two
+        const float top = fmaxf(sc.v[0], sc.v[1]), low = fminf(sc.v[0], sc.v[1]);
+        const bool wide = kPer == 2 && low > 0.f && top > 64.f * low;  // (uniform)
+        auto tile_max = [&](int i) {  // of heads 4 i ..
+            float4 m = *reinterpret_cast<const float4 *>(now_m + 4 * i);
+            if (kPer == 2) {
+                const float4 n = *reinterpret_cast<const float4 *>(now_m + NH + 4 * i);
+                m.x = fmaxf(m.x, n.x), m.y = fmaxf(m.y, n.y), m.z = fmaxf(m.z, n.z), m.w = fmaxf(m.w, n.w);
+            }
+            return m;
+        };
+        // (wide) log2 of the largest product of weight and value scale of head h, weights against maximum m
+        const float log0 = wide ? __log2f(sc.v[0]) : 0.f, log1 = wide ? __log2f(sc.v[1]) : 0.f;
+        auto largest = [&](int h, float m) { return fmaxf(log0 + (now_m[h] - m), log1 + (now_m[NH + h] - m)); };
         {
+            const float unit = kPer == 1 ? 256.f : top > 0.f ? 256.f * ((tid < S ? sc.v[0] : sc.v[1]) / top) : 0.f;
             const uint64_t unit2 = f2_pack(unit, unit);
 #pragma unroll
             for (int i = 0; i < NH / 4; ++i) {
-                const float4 m = *reinterpret_cast<const float4 *>(now_m + 4 * i);
-                const float4 old = *reinterpret_cast<const float4 *>(old_m + 4 * i);
-                grown |= m.x != old.x || m.y != old.y || m.z != old.z || m.w != old.w;
+                const float4 m = tile_max(i);
                 float a[4];
                 f2_unpack(fadd2(p[2 * i], f2_pack(-m.x, -m.y)), a[0], a[1]);
                 f2_unpack(fadd2(p[2 * i + 1], f2_pack(-m.z, -m.w)), a[2], a[3]);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) sum[4 * i + e] = fast_exp2(a[e]);  // 0 for a masked key
-                p[2 * i] = fmul2(f2_pack(sum[4 * i], sum[4 * i + 1]), unit2);
-                p[2 * i + 1] = fmul2(f2_pack(sum[4 * i + 2], sum[4 * i + 3]), unit2);
+                if (!wide) {
+                    p[2 * i] = fmul2(f2_pack(sum[4 * i], sum[4 * i + 1]), unit2);
+                    p[2 * i + 1] = fmul2(f2_pack(sum[4 * i + 2], sum[4 * i + 3]), unit2);
+                } else {
+                    const float mm[4] = {m.x, m.y, m.z, m.w}, own = (tid < S ? log0 : log1) + 8.f;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) a[e] = fast_exp2(a[e] + (own - largest(4 * i + e, mm[e])));
+                    p[2 * i] = f2_pack(a[0], a[1]);
+                    p[2 * i + 1] = f2_pack(a[2], a[3]);
+                }
             }
         }
-        if (grown) {  // (uniform) the outputs so far are brought to the new maxima
-#pragma unroll
-            for (int i = 0; i < NH / 4; ++i) {
-                const float4 m = *reinterpret_cast<const float4 *>(now_m + 4 * i);
-                const float4 old = *reinterpret_cast<const float4 *>(old_m + 4 * i);
-                o[2 * i] = fmul2(o[2 * i], f2_pack(fast_exp2(old.x - m.x), fast_exp2(old.y - m.y)));
-                o[2 * i + 1] = fmul2(o[2 * i + 1], f2_pack(fast_exp2(old.z - m.z), fast_exp2(old.w - m.w)));
-            }
+        float m_tile = 0.f, own_f = 0.f, old_f = 0.f;  // (threads below NH)
+        if (tid < NH) {
+            m_tile = kPer == 2 ? fmaxf(now_m[tid], now_m[NH + tid]) : now_m[tid];
+            const float m = fmaxf(m_run, m_tile);
+            old_f = fast_exp2(m_run - m);
+            own_f = fast_exp2(m_tile - m);
+            m_run = m;
+            head_old[tid] = old_f;
+            head_new[tid] = wide ? fast_exp2(m_tile - m + (largest(tid, m_tile) - 8.f)) : own_f * (top * (1.f / 256.f));
         }
         // sums over the warp: each step hands a lane half of the heads it holds
         {
@@ -611,7 +636,7 @@ __global__ void __launch_bounds__(128, CacheAttend<NH>::kPerSm) cache_attend_ker
         }
         fence_proxy_async_smem();
         tc_fence_before();
-        if (__syncthreads_or(!ok)) {
+        if (__syncthreads_or(!ok || failed)) {
             leave(true);
             return;
         }
@@ -630,21 +655,22 @@ __global__ void __launch_bounds__(128, CacheAttend<NH>::kPerSm) cache_attend_ker
         // meanwhile: the head's running maximum and sum, and the blocks' own
         if (tid < NH) {
             const float4 rl = *reinterpret_cast<const float4 *>(red_l + tid * 4);
-            const float m = now_m[tid], l = (rl.x + rl.y) + (rl.z + rl.w);
-            head_l[tid] = head_l[tid] * fast_exp2(head_old - m) + l;
-            // the next tile's maxima start from these; others may have begun to raise them
-            atomic_max_shared(old_m + tid, m);
+            const float l = (rl.x + rl.y) + (rl.z + rl.w);
+            l_run = l_run * old_f + l * own_f;
+            float *later = tile_m + (turn == 0 ? 2 : turn - 1) * 2 * NH + tid;  // those of the tile after the next
+            later[0] = later[NH] = kLowest;
             if (block_ml && tid < G) {
                 float2 *to = block_ml + (static_cast<size_t>(bh) * G + tid) * (k > 0 ? k : nb) + cur.t * kPer;
                 if (kPer == 1) {
-                    to[0] = make_float2(m, l);
+                    to[0] = make_float2(m_tile, l);
                 } else {
-                    to[0] = make_float2(m, rl.x + rl.y);
-                    if (blk.v[kPer - 1] >= 0) to[1] = make_float2(m, rl.z + rl.w);
+                    to[0] = make_float2(m_tile, rl.x + rl.y);
+                    if (blk.v[kPer - 1] >= 0) to[1] = make_float2(m_tile, rl.z + rl.w);
                 }
             }
         }
-        ok = mbar_wait(bar_o, ph, abort_flag, 0x714);  // (a failure is met at the next tile's barrier, or below)
+        ok = mbar_wait(bar_o, ph, abort_flag, 0x714);
+        failed = !ok;  // (met at the next tile's barrier, or at the end)
         tc_fence_after();
         if (tid == kLoader && ok && it + 1 < n_tiles) {  // the values have been read
             load(&mapV, bar_v, SM::kTile, pos1, blk1);
@@ -652,13 +678,14 @@ __global__ void __launch_bounds__(128, CacheAttend<NH>::kPerSm) cache_attend_ker
         }
         {
             const uint32_t row = tmem + SM::kTmemO + (static_cast<uint32_t>(warp * 32) << 16);
-            const float back = sc.top * (1.f / 256.f);
-            const uint64_t back2 = f2_pack(back, back), sixteenth = f2_pack(0.0625f, 0.0625f);
+            const uint64_t sixteenth = f2_pack(0.0625f, 0.0625f);
+            auto factor = [&](const float *f, int i) { return *reinterpret_cast<const uint64_t *>(f + 2 * i); };
             auto add = [&](const float *t0, const float *t1, const float *t2) {
 #pragma unroll
                 for (int i = 0; i < NH / 2; ++i) {
                     const uint64_t a = ffma2(f2_pack(t2[2 * i], t2[2 * i + 1]), sixteenth, f2_pack(t1[2 * i], t1[2 * i + 1]));
-                    o[i] = ffma2(ffma2(a, sixteenth, f2_pack(t0[2 * i], t0[2 * i + 1])), back2, o[i]);
+                    o[i] = ffma2(ffma2(a, sixteenth, f2_pack(t0[2 * i], t0[2 * i + 1])), factor(head_new, i),
+                                 fmul2(o[i], factor(head_old, i)));
                 }
             };
             if constexpr (NH == 4) {
@@ -675,23 +702,23 @@ __global__ void __launch_bounds__(128, CacheAttend<NH>::kPerSm) cache_attend_ker
                 tmem_ld16(row + 32, w);
                 add(v, v + 16, w);
             } else {
-                float f = back;
+                uint64_t acc[16];
 #pragma unroll
-                for (int term = 0; term < 3; ++term, f *= 0.0625f) {
+                for (int term = 2; term >= 0; --term) {
                     float v[32];
                     tmem_ld32(row + 32 * term, v);
-                    const uint64_t f2 = f2_pack(f, f);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) o[i] = ffma2(f2_pack(v[2 * i], v[2 * i + 1]), f2, o[i]);
+                    for (int i = 0; i < 16; ++i) {
+                        const uint64_t x = f2_pack(v[2 * i], v[2 * i + 1]);
+                        acc[i] = term == 2 ? x : ffma2(acc[i], sixteenth, x);
+                    }
                 }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] = ffma2(acc[i], factor(head_new, i), fmul2(o[i], factor(head_old, i)));
             }
             tc_fence_before();
         }
         if (last) {
-            if (__syncthreads_or(!ok)) {  // (also: head_m and head_l are complete)
-                leave(true);
-                return;
-            }
             const size_t slot = static_cast<size_t>(blockIdx.x) + bh;
             float *to = opart + slot * G * kCacheD + tid;
 #pragma unroll
@@ -701,8 +728,7 @@ __global__ void __launch_bounds__(128, CacheAttend<NH>::kPerSm) cache_attend_ker
                 if (2 * i < G) to[2 * i * kCacheD] = a;
                 if (2 * i + 1 < G) to[(2 * i + 1) * kCacheD] = c;
             }
-            if (tid < G) mlpart[slot * G + tid] = make_float2(now_m[tid], head_l[tid]);
-            __syncthreads();  // head_* are set anew for the next pair
+            if (tid < G) mlpart[slot * G + tid] = make_float2(m_run, l_run);
         } else if (!SM::kApart) {
             __syncthreads();  // every warp has read its outputs before the next logits take their place
         }
@@ -711,8 +737,9 @@ __global__ void __launch_bounds__(128, CacheAttend<NH>::kPerSm) cache_attend_ker
         blk = blk1;
         blk1 = blk2;
         sc = sc1;
+        turn = turn == 2 ? 0 : turn + 1;
     }
-    leave(false);
+    leave(__syncthreads_or(failed) != 0);
 }
 
 // ---------------------------------------------------------------------------

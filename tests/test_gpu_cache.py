@@ -6,8 +6,14 @@ fp32 sum of s codes: 32 * 2^-24 of the mean magnitude.  A logit is a sum of 2 d
 exact products in fp32 of a query in two terms: 2^-20 of the sum of magnitudes it
 is made of, and its exponential carries that as a relative error, as do the
 weights and, in absolute terms, lse.  The output's weights are further cut to
-three terms of 4 bits (2^-13 of the weight, 2^-26 of the largest) and it is rounded
-to bf16 (2^-8 of its value)."""
+three terms of 4 significant bits and it is rounded to bf16 (2^-8 of its value).
+A rounding to 4 significant bits is off by at most 2^-4 of the value, and each term
+holds what the ones before it left: (2^-4)^3 = 2^-12 of the weight; where the third
+term is below 2^-6, half its step of 2^-9 counts, 2^-10 / (256 * 256) = 2^-26 of the
+unit that stands for 256.  That is the largest weight of the key's tile of 128 keys
+(one block of 128, two of 64) times the tile's larger value scale, at most 2^6 times
+the key's own (2^-20 of the value), or else the tile's largest product of weight and
+value scale (2^-26 of it times the key's code)."""
 import numpy as np
 import pytest
 
@@ -197,8 +203,14 @@ def check_decode(dims, c, lens, q, out, weight_in=None, weight_out=None, rows=No
         ro, rl, p, size = R.attend(qn[b, heads], Kd, Vd, tokens, dims.scale)
         e = 2.0 ** -20 * (size + 1.0)[:, None]
         spread = p @ np.abs(Vd[tokens])
-        tol = (2.0 ** -8 * np.abs(ro) + (2.0 ** -13 + 2 * e) * spread
-               + 2.0 ** -26 * p.max(1, keepdims=True) * np.abs(Vd[tokens]).sum(0))
+        tol = 2.0 ** -8 * np.abs(ro) + (2.0 ** -12 + 2 * e) * spread
+        slots = np.concatenate([np.full(min((j + 1) * s, Lb + 1) - j * s, i) for i, j in enumerate(blocks)])
+        vs = Vs[b, h].astype(np.float64)[tokens // s]
+        for tile in range(slots[-1] // (128 // s) + 1):
+            u = np.flatnonzero(slots // (128 // s) == tile)
+            V = np.abs(Vd[tokens[u]])
+            tol += np.maximum(2.0 ** -20 * p[:, u].max(1, keepdims=True) * V.sum(0),
+                              2.0 ** -26 * (p[:, u] * vs[u]).max(1, keepdims=True) * (V / vs[u][:, None]).sum(0))
         assert np.all(np.abs(o[b, heads] - ro) <= tol), (b, h, np.max(np.abs(o[b, heads] - ro) / tol))
         assert np.all(np.abs(lse[b, heads] - rl) <= e[:, 0] + 2.0 ** -22 * np.abs(rl))
         if weight_out is not None:
@@ -209,7 +221,8 @@ def check_decode(dims, c, lens, q, out, weight_in=None, weight_out=None, rows=No
                 add[j] = p[:, m].sum()
                 slack[j] = (2 * e[:, 0] * p[:, m].sum(1)).sum()
             got = weight_out[b, h].double().cpu().numpy()
-            assert np.all(np.abs(got - (win + add)) <= slack + 2.0 ** -22 * (win + add))
+            # (weights below 2^-126, the smallest normal fp32, count as 0: at most so much for each of s keys and G heads)
+            assert np.all(np.abs(got - (win + add)) <= slack + 2.0 ** -22 * (win + add) + s * G * 2.0 ** -126)
 
 
 def query(B, H, seed=7, size=2.0):
@@ -308,6 +321,31 @@ def test_decode_extreme_values():
     o, lse, _ = out
     assert bool(o[3, :3].isnan().all()) and bool(lse[3, :3].isnan().all())  # the head with the NaN key, the NaN query
     assert bool(o[3, 3].isfinite().all()) and bool(lse[3, 3].isfinite())    # its neighbour is untouched
+
+
+@pytest.mark.parametrize("s", [64, 128])
+def test_decode_value_scales_far_apart(s):
+    """Value scales from 2^-40 to 2^40 from block to block, and logits up to tens apart: the blocks that carry the
+    weight and those that carry the output are others, and both keep their precision."""
+    T = 16 * s
+    lens = [T - 1, 9 * s + 5, 3 * s - 1, 2 * s]
+    dims = L.make_dims(4, 8, T, D, s, 0, Hkv=4)
+    c = filled(dims, lens, seed=3)
+    c.Vscale.mul_(torch.exp2(torch.randint(-40, 41, c.Vscale.shape, device="cuda", generator=gen(4)).float()))
+    for size in (0.5, 2.0, 12.0):
+        q = query(4, 8, 5, size)
+        w = torch.empty(4, 4, T // s, device="cuda")
+        out = ops.cache_decode(dims, c, i32(*lens), q, weight_out=w)
+        check_decode(dims, c, lens, q, out, None, w)
+    # one block's values vanish beside the other's in the same tile, and it has all the weight
+    c.Vscale[:, :, 1::2] = c.Vscale[:, :, ::2] * 2.0 ** 30
+    q = query(4, 8, 6, 1.0)
+    K8 = torch.zeros(4, 4, T, D, device="cuda")
+    K8[:, :, (torch.arange(T, device="cuda") // s) % 2 == 0] = torch.sign(q.float().view(4, 4, 2, D).sum(2))[:, :, None]
+    c.K8.copy_(K8.to(torch.float8_e4m3fn))
+    c.Kscale.fill_(4.0)
+    out = ops.cache_decode(dims, c, i32(*lens), q)
+    check_decode(dims, c, lens, q, out)
 
 
 def test_decode_reports_bad_lengths():
