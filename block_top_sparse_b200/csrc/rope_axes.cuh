@@ -12,8 +12,8 @@
 // (cos(a + e) = cos a - e sin a): no range reduction of a large angle, and an
 // error of the order of fp32's own rounding at any 32-bit position.
 //
-// One CTA per `rows` consecutive tokens (flattened over the sequences) and
-// slice of heads: the tokens' cosines and sines are computed once, while the
+// One CTA per `rows` consecutive tokens (flattened over the sequences): the
+// tokens' cosines and sines are computed once, while the
 // first heads' rows are on their way.  A thread keeps those of one token's
 // 16-byte piece in registers and walks down the heads with them, four heads'
 // loads (both halves of the row) in flight.
@@ -69,11 +69,11 @@ __device__ __forceinline__ uint4 rope_pack(const float (&v)[16 / sizeof(T)]) {
     return make_uint4(p[0], p[1], p[2], p[3]);
 }
 
-// grid (ceil(B*T / rows), head slices); heads_per = query heads, then key heads, of one slice.
+// grid ceil(B*T / rows).
 template <typename T>
 __global__ void __launch_bounds__(kRopeAxesThreads, 3) rope_axes_kernel(
     const __grid_constant__ RopeAxesTable tab, const int32_t *__restrict__ pos, int64_t BT, int T_len, int half,
-    int rows, int heads_per, float sign, const __grid_constant__ RopeAxesTensor Q,
+    int rows, float sign, const __grid_constant__ RopeAxesTensor Q,
     const __grid_constant__ RopeAxesTensor K) {
     constexpr int V = 16 / sizeof(T), U = 4;
     __shared__ float2 cs[kRopeAxesRows][64];
@@ -83,8 +83,8 @@ __global__ void __launch_bounds__(kRopeAxesThreads, 3) rope_axes_kernel(
     // heads come first, then the keys'
     const int units = half / V, u = threadIdx.x % units, tt = threadIdx.x / units % rows;
     const int step = kRopeAxesThreads / units / rows;
-    const int h1 = min((static_cast<int>(blockIdx.y) + 1) * heads_per, Q.heads + K.heads);
-    int h = blockIdx.y * heads_per + threadIdx.x / units / rows;
+    const int h1 = Q.heads + K.heads;
+    int h = threadIdx.x / units / rows;
     if (tt >= nt) h = h1;
     const int64_t f = f0 + tt, b = f / T_len, t = f % T_len;
     const T *q_in = static_cast<const T *>(Q.in) + b * Q.is[0] + t * Q.is[2] + u * V;

@@ -927,22 +927,16 @@ ssa_status_t ssa_rope_axes(const ssa_dims_t *dims, const int32_t *pos, int axes,
     for (int i = half; i < 64; ++i) tab.axis[i] = 0, tab.turns[i] = 0.0;
     // tokens per CTA: 8 where there are many (16: 118 and 49 us instead of 115 and 46 us for 32K tokens of 40 bf16
     // heads of 128 and 16K of 32 fp32 heads of 64, whose last wave is longer), down to one, so that at
-    // least two CTAs per SM share the work; then the heads are split while SMs are still idle
-    const int heads = XQ.heads + XK.heads;
+    // least two CTAs per SM share the work
     int rows = 1;
     while (rows < kRopeAxesRows && BT > static_cast<int64_t>(rows) * 2 * kCacheSms) rows *= 2;
-    const int64_t ctas = (BT + rows - 1) / rows;
-    int slices = static_cast<int>(2 * kCacheSms / ctas);
-    slices = slices < 1 ? 1 : slices > (heads + 7) / 8 ? (heads + 7) / 8 : slices;
-    const int per_slice = (heads + slices - 1) / slices;
-    const dim3 grid(static_cast<unsigned>(ctas), (heads + per_slice - 1) / per_slice);
+    const unsigned grid = static_cast<unsigned>((BT + rows - 1) / rows);
     const float sign = (flags & SSA_ROPE_TRANSPOSE) ? -1.f : 1.f;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (dims->dtype == SSA_DT_BF16)
-        rope_axes_kernel<__nv_bfloat16><<<grid, kRopeAxesThreads, 0, st>>>(tab, pos, BT, T, half, rows, per_slice, sign, XQ,
-                                                                           XK);
+        rope_axes_kernel<__nv_bfloat16><<<grid, kRopeAxesThreads, 0, st>>>(tab, pos, BT, T, half, rows, sign, XQ, XK);
     else
-        rope_axes_kernel<float><<<grid, kRopeAxesThreads, 0, st>>>(tab, pos, BT, T, half, rows, per_slice, sign, XQ, XK);
+        rope_axes_kernel<float><<<grid, kRopeAxesThreads, 0, st>>>(tab, pos, BT, T, half, rows, sign, XQ, XK);
     return launch_status();
 }
 
@@ -1009,7 +1003,8 @@ ssa_status_t ssa_cache_decode(const ssa_dims_t *dims, const int32_t *cache_len, 
     CUtensorMap tmK, tmV;
     if (!make_tmap_codes(&tmK, K8, S.krows, S.s) || !make_tmap_codes(&tmV, V8, S.krows, S.s)) return SSA_ERR_CUDA;
     if (S.k > 0) {
-        // CTAs per pair: a second one only from 128 blocks on (each scores 64 at a time), while SMs are idle
+        // CTAs per pair: a second one only from 128 blocks on (each scores 64 at a time), while SMs are idle: one
+        // sequence of 131072 tokens, 8 key heads, 32 blocks of 128: 25 us in all with one CTA per pair, 19 us with eight
         unsigned parts = 1;
         while (parts < 8 && parts * 2 * bhk <= 2u * kCacheSms && static_cast<unsigned>(S.nb) >= 128 * parts) parts *= 2;
         cudaLaunchAttribute attr[1];
@@ -1060,11 +1055,9 @@ ssa_status_t ssa_cache_decode(const ssa_dims_t *dims, const int32_t *cache_len, 
                                 : cache_combine_kernel<4>;
     const unsigned head_ctas = split ? split * static_cast<unsigned>(S.BH) : bhk * ((S.G + 7) / 8);
     const size_t weight_ctas = split && weight_out ? S.BHk * ((S.nb + 255) / 256) : 0;
-    // (four warps are enough for up to four heads, and more of the small CTAs start beside the attention's)
-    if (!launch_dependent(combine, dim3(static_cast<unsigned>(head_ctas + weight_ctas)), split == 0 && S.G <= 4 ? 128 : 256,
-                          0, st, cache_len, opart, ml, block_ml, idx, static_cast<__nv_bfloat16 *>(o), lse, weight_in,
-                          weight_out, S.B, S.Hk, S.G, S.T, S.s, S.k, S.nb, static_cast<int>(grid),
-                          static_cast<int>(head_ctas)))
+    if (!launch_dependent(combine, dim3(static_cast<unsigned>(head_ctas + weight_ctas)), 256, 0, st, cache_len, opart, ml,
+                          block_ml, idx, static_cast<__nv_bfloat16 *>(o), lse, weight_in, weight_out, S.B, S.Hk, S.G, S.T,
+                          S.s, S.k, S.nb, static_cast<int>(grid), static_cast<int>(head_ctas)))
         return SSA_ERR_CUDA;
     return launch_status();
 }

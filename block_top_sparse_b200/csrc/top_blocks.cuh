@@ -113,7 +113,8 @@ __device__ __forceinline__ void top_ascending(const uint32_t *keys, int n, int k
 // The same for n < 1024 by one warp, the keys in its registers (KPL per lane, n <= 32 * KPL): the kk-th
 // largest key is found two bits at a time from the first bit in which the keys differ (three candidates'
 // counts, 11 bits each, in one warp sum), stopping early at a candidate with exactly kk keys at or above it.
-// No barrier; a third of the time of the CTA's counts for 256 keys.
+// No barrier.  (Eviction of one of 17 blocks 7.7 us in all, selection of 16 of up to 256 blocks in 512 rows
+// 15.6 us; with the CTA's counts 9.0 and 16.4 us.)
 template <int KPL>
 __device__ __forceinline__ void top_ascending_warp(const uint32_t *keys, int n, int kk, int32_t *out, int lane) {
     uint32_t key[KPL], hi = 0u, lo = 0xFFFFFFFFu;

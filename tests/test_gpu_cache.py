@@ -323,25 +323,26 @@ def test_decode_extreme_values():
     assert bool(o[3, 3].isfinite().all()) and bool(lse[3, 3].isfinite())    # its neighbour is untouched
 
 
+@pytest.mark.parametrize("G", [2, 8, 13, 32])
 @pytest.mark.parametrize("s", [64, 128])
-def test_decode_value_scales_far_apart(s):
+def test_decode_value_scales_far_apart(s, G):
     """Value scales from 2^-40 to 2^40 from block to block, and logits up to tens apart: the blocks that carry the
     weight and those that carry the output are others, and both keep their precision."""
     T = 16 * s
     lens = [T - 1, 9 * s + 5, 3 * s - 1, 2 * s]
-    dims = L.make_dims(4, 8, T, D, s, 0, Hkv=4)
+    dims = L.make_dims(4, 4 * G, T, D, s, 0, Hkv=4)
     c = filled(dims, lens, seed=3)
     c.Vscale.mul_(torch.exp2(torch.randint(-40, 41, c.Vscale.shape, device="cuda", generator=gen(4)).float()))
     for size in (0.5, 2.0, 12.0):
-        q = query(4, 8, 5, size)
+        q = query(4, 4 * G, 5, size)
         w = torch.empty(4, 4, T // s, device="cuda")
         out = ops.cache_decode(dims, c, i32(*lens), q, weight_out=w)
         check_decode(dims, c, lens, q, out, None, w)
     # one block's values vanish beside the other's in the same tile, and it has all the weight
     c.Vscale[:, :, 1::2] = c.Vscale[:, :, ::2] * 2.0 ** 30
-    q = query(4, 8, 6, 1.0)
+    q = query(4, 4 * G, 6, 1.0)
     K8 = torch.zeros(4, 4, T, D, device="cuda")
-    K8[:, :, (torch.arange(T, device="cuda") // s) % 2 == 0] = torch.sign(q.float().view(4, 4, 2, D).sum(2))[:, :, None]
+    K8[:, :, (torch.arange(T, device="cuda") // s) % 2 == 0] = torch.sign(q.float().view(4, 4, G, D).sum(2))[:, :, None]
     c.K8.copy_(K8.to(torch.float8_e4m3fn))
     c.Kscale.fill_(4.0)
     out = ops.cache_decode(dims, c, i32(*lens), q)
