@@ -244,9 +244,9 @@ struct CacheAttend {
     static constexpr int kTmemO = kApart ? kNS : 0;                  // first column of the output's product
     static constexpr int kCols = kTmemO + kNP;
     static constexpr int kTmemCols = kCols <= 32 ? 32 : kCols <= 64 ? 64 : 128;
-    // CTAs per SM: shared memory (33 KB of keys and values and 4 to 20 KB of operands each) and, from NH = 16
-    // on, registers and tensor memory
-    static constexpr int kPerSm = NH <= 8 ? 5 : NH == 16 ? 4 : 3;
+    // CTAs per SM.  64 caches of 16K to 32K tokens, 8 key heads, G = 4: 459 us with three, 458 us with four, 473 us
+    // with five; 16 ragged ones, G = 8, blocks of 64: 45, 35 and 35 us.  NH = 32 has registers for three.
+    static constexpr int kPerSm = NH <= 16 ? 4 : 3;
 };
 
 // Tile of 128 keys (one block of 128 or two of 64):
@@ -258,9 +258,9 @@ struct CacheAttend {
 // of the largest product of weight and scale.  The outputs stay in registers, brought to the running maximum tile
 // by tile; only O^T of one tile is in tensor memory.  A tile is a chain of dependent steps (product, maximum, weights, product, output), so the CTA is
 // kept small -- one tile of keys and one of values, each loaded again as soon as its product has read it --
-// and up to five CTAs per SM run their chains beside one another's loads: 160 KB in flight or in use per SM.
+// and up to four CTAs per SM run their chains beside one another's loads: 128 KB in flight or in use per SM.
 // (Two tiles of each and three CTAs per SM: 784 us instead of 481 us for 64 caches of 16K to 32K tokens, 8 key
-// heads, G = 4; 472 us, 6.8 TB/s, with the steps since.)
+// heads, G = 4; 458 us, 7.0 TB/s, with the steps since.)
 template <int NH, int S>
 __global__ void __launch_bounds__(128, CacheAttend<NH>::kPerSm) cache_attend_kernel(
     const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
@@ -286,8 +286,8 @@ __global__ void __launch_bounds__(128, CacheAttend<NH>::kPerSm) cache_attend_ker
     volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + 5);
 
     // Tensor memory first: the SM starts its next CTA only when this one has given up the right to allocate
-    // (measured: with the allocation behind the search below the fifth CTA of an SM started 7.4 us after the first,
-    // now 2.2 us; 16 ragged sequences of up to 32K tokens 38 -> 36 us in all).
+    // (measured with five: with the allocation behind the search below the fifth CTA of an SM started 7.4 us after
+    // the first, now 2.2 us; 16 ragged sequences of up to 32K tokens 38 -> 36 us in all).
     if (warp == 1) {
         tmem_alloc(tmem_slot, SM::kTmemCols);
         tmem_relinquish();
