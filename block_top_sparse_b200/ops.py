@@ -127,12 +127,12 @@ def rope_axes(dims: L.Dims, pos: torch.Tensor, sections, Q: torch.Tensor, K: Opt
     out: the pair of tensors to write, (Q, K) for in place; default: new contiguous ones.  Returns (Qr, Kr)."""
     dev = _device_of(Q)
     dtype = Q.dtype
-    if dtype not in (torch.bfloat16, torch.float32):
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
         raise ValueError("Q must be bf16 or fp32, got %s" % dtype)
-    shape = (dims.B, dims.H, dims.T, dims.d)
-    kshape = (dims.B, dims.kv_heads, dims.T, dims.d)
+    B, H, T, d, Hk = dims.B, dims.H, dims.T, dims.d, dims.Hkv or dims.H
+    shape, kshape = (B, H, T, d), (B, Hk, T, d)
     _is(Q, "Q", shape, dtype, dev, True)
-    _is(pos, "pos", (len(sections), dims.B, dims.T), torch.int32, dev)
+    _is(pos, "pos", (len(sections), B, T), torch.int32, dev)
     if K is not None:
         _is(K, "K", kshape, dtype, dev, True)
     if out is None:
@@ -144,11 +144,12 @@ def rope_axes(dims: L.Dims, pos: torch.Tensor, sections, Q: torch.Tensor, K: Opt
             raise ValueError("out must hold a tensor for K exactly when K is given")
         if Kr is not None:
             _is(Kr, "out[1]", kshape, dtype, dev, True)
-    d = L.Dims(dims.B, dims.H, dims.T, dims.d, dims.s, dims.k,
-               L.SSA_DT_FP32 if dtype == torch.float32 else L.SSA_DT_BF16, dims.scale, dims.Hkv)
+    own = L.SSA_DT_FP32 if dtype is torch.float32 else L.SSA_DT_BF16
+    if dims.dtype != own:
+        dims = L.Dims(B, H, T, d, dims.s, dims.k, own, dims.scale, dims.Hkv)
     flags = ((L.SSA_ROPE_TRANSPOSE if transpose else 0) | (L.SSA_ROPE_INTERLEAVED if interleaved else 0)
              | (L.SSA_ROPE_OWN_LADDER if own_ladder else 0))
-    L.ssa_rope_axes(d, pos, sections, Q, Qr, K, Kr, flags, base, factor)
+    L.ssa_rope_axes(dims, pos, sections, Q, Qr, K, Kr, flags, base, factor)
     return Qr, Kr
 
 
@@ -193,13 +194,15 @@ def cache_append(dims: L.Dims, cache: Cache8, cache_len: torch.Tensor, K: torch.
     """Writes the tokens K, V [B, Hkv, n, d] (bf16, also strided views) at cache_len [B] (int32) of every sequence,
     n_new[b] of them (default: n).  The caller advances cache_len, once for all layers."""
     dev = _device_of(K)
-    shape = (dims.B, dims.kv_heads, K.shape[2], dims.d)
+    B, Hk, _ = cache.check(dims, dev)
+    if K.dim() != 4:
+        raise ValueError("K must be [B, Hkv, n, d], got %s" % list(K.shape))
+    shape = (B, Hk, K.shape[2], dims.d)
     _is(K, "K", shape, torch.bfloat16, dev, True)
     _is(V, "V", shape, torch.bfloat16, dev, True)
-    _is(cache_len, "cache_len", (dims.B,), torch.int32, dev)
+    _is(cache_len, "cache_len", (B,), torch.int32, dev)
     if n_new is not None:
-        _is(n_new, "n_new", (dims.B,), torch.int32, dev)
-    cache.check(dims, dev)
+        _is(n_new, "n_new", (B,), torch.int32, dev)
     L.ssa_cache_append(dims, cache_len, K, V, cache.K8, cache.Kscale, cache.V8, cache.Vscale, cache.Kbar, n_new)
 
 
@@ -211,16 +214,18 @@ def cache_decode(dims: L.Dims, cache: Cache8, cache_len: torch.Tensor, q: torch.
     every block's attention weight; the same tensor for both adds in place.  Returns (o, lse, idx); idx is None for
     dims.k == 0."""
     dev = _device_of(q)
-    _is(q, "q", (dims.B, dims.H, dims.d), torch.bfloat16, dev)
-    _is(cache_len, "cache_len", (dims.B,), torch.int32, dev)
     scales = cache.check(dims, dev)
+    B, Hk, _ = scales
+    H, k = dims.H, dims.k
+    _is(q, "q", (B, H, dims.d), torch.bfloat16, dev)
+    _is(cache_len, "cache_len", (B,), torch.int32, dev)
     if weight_in is not None:
         _is(weight_in, "weight_in", scales, torch.float32, dev)
     if weight_out is not None:
         _is(weight_out, "weight_out", scales, torch.float32, dev)
     o = torch.empty_like(q)
-    lse = cache.Kscale.new_empty((dims.B, dims.H))
-    idx = cache_len.new_empty((dims.B, dims.kv_heads, dims.k)) if dims.k > 0 else None
+    lse = cache.Kscale.new_empty((B, H))
+    idx = cache_len.new_empty((B, Hk, k)) if k > 0 else None
     if ws is None:
         ws = _ws(dims, L.SSA_OP_CACHE_DECODE, q.device)
     elif ws.get_device() != dev or not ws.is_contiguous():
@@ -237,16 +242,17 @@ def cache_evict(dims: L.Dims, cache: Cache8, cache_len: torch.Tensor, keep: int,
     ones of greatest weight [B, Hkv, T/s]; the cache is compacted in place.  weight_out (may be weight) receives the
     weights in the new order, new_len (default: a new tensor; may be cache_len) the lengths.  Returns (kept, new_len)."""
     dev = _device_of(weight)
-    _is(cache_len, "cache_len", (dims.B,), torch.int32, dev)
     scales = cache.check(dims, dev)
+    B, Hk, _ = scales
+    _is(cache_len, "cache_len", (B,), torch.int32, dev)
     _is(weight, "weight", scales, torch.float32, dev)
     if weight_out is not None:
         _is(weight_out, "weight_out", scales, torch.float32, dev)
     if new_len is None:
         new_len = torch.empty_like(cache_len)
     else:
-        _is(new_len, "new_len", (dims.B,), torch.int32, dev)
-    kept = cache_len.new_empty((dims.B, dims.kv_heads, max(int(keep), 0)))
+        _is(new_len, "new_len", (B,), torch.int32, dev)
+    kept = cache_len.new_empty((B, Hk, max(int(keep), 0)))
     if ws is None:
         ws = _ws(dims, L.SSA_OP_CACHE_EVICT, weight.device)
     elif ws.get_device() != dev or not ws.is_contiguous():
