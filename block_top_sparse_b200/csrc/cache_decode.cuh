@@ -15,8 +15,10 @@
 // terms of 4 significant bits each:
 //   q = 2^e (t0 + t1/16):          8 significant bits (bf16) in two terms, or 2^-22 of the
 //                                  head's largest element,
-//   p = (t0 + t1/16 + t2/256)/256: 12 bits, error <= 2^-12 p (three roundings, each at
-//                                  most 2^-4 of what is left) + 2^-26 of a tile's largest.
+//   p = (t0 + t1/16 + t2/256 + t3/4096)/256: 16 bits, error <= 2^-16 p (four roundings,
+//                                  each at most 2^-4 of what is left) + 2^-30 of a tile's largest.
+// (Three terms, 12 bits, showed where values cancel: with weights 2^-10 apart, what is left was off by up to
+// 2^-2.6 of itself, now by 2^-8 with its rounding to bf16.)
 // The terms are extra columns (N) of the same product, and its results are put
 // together in fp32; N is small and the tensor cores have time to spare.
 //
@@ -231,7 +233,7 @@ template <int NH>
 struct CacheAttend {
     static constexpr int kTile = 128 * kCacheD;                      // 16 KB: keys or values of one tile
     static constexpr int kNS = NH < 8 ? 16 : 2 * NH;                 // columns of the logits' product (term * NH + head)
-    static constexpr int kNP = (3 * NH + 15) / 16 * 16;              // columns of the output's product
+    static constexpr int kNP = 4 * NH;                               // columns of the output's product
     static constexpr int kQ = 2 * kTile;                             // [kNS][128 B]
     static constexpr int kP = kQ + kNS * 128;                        // [kNP / 16][128 keys][16 B]
     static constexpr int kRed = kP + kNP * 128;                      // two of: [NH][4 warps] sums
@@ -239,7 +241,7 @@ struct CacheAttend {
     static constexpr int kBar = kHead + 9 * NH * 4;
     static constexpr int kBytes = kBar + 64 + 1024;                  // + alignment of the dynamic base to 1024 B
     // the logits' columns may be written again while the outputs are read, except at NH = 32, where both
-    // products would take 256 columns a CTA and the outputs take the logits' place
+    // products would take 192 columns a CTA (256 allocated) and the outputs take the logits' place
     static constexpr bool kApart = NH < 32;
     static constexpr int kTmemO = kApart ? kNS : 0;                  // first column of the output's product
     static constexpr int kCols = kTmemO + kNP;
@@ -251,9 +253,9 @@ struct CacheAttend {
 
 // Tile of 128 keys (one block of 128 or two of 64):
 //   S^T [128 keys x 2 NH] = K8 . (q terms)^T      A: keys as loaded (K-major), thread = key
-//   weights of the thread's key against the tile's maxima, split into three terms
-//   O^T [128 dims x 3 NH] = V8^T . (p terms)^T    A: values as loaded (M-major), thread = dim
-// A tile's weights are relative to its own maximum, so their 2^-26 is of the tile's largest weight, however much
+//   weights of the thread's key against the tile's maxima, split into four terms
+//   O^T [128 dims x 4 NH] = V8^T . (p terms)^T    A: values as loaded (M-major), thread = dim
+// A tile's weights are relative to its own maximum, so their 2^-30 is of the tile's largest weight, however much
 // larger another tile's is; where the values of two blocks of 64 in a tile have scales more than 2^6 apart, it is
 // of the largest product of weight and scale.  The outputs stay in registers, brought to the running maximum tile
 // by tile; only O^T of one tile is in tensor memory.  A tile is a chain of dependent steps (product, maximum, weights, product, output), so the CTA is
@@ -603,7 +605,7 @@ __global__ void __launch_bounds__(128, CacheAttend<NH>::kPerSm) cache_attend_ker
             constexpr int kLanes = 32 / NH;  // lanes that end up with the same head
             if (lane % kLanes == 0) red_l[lane / kLanes * 4 + warp] = sum[0];
         }
-        // three terms of every weight into the N-major operand: byte term * NH + h of the key's row, rows of 16
+        // four terms of every weight into the N-major operand: byte term * NH + h of the key's row, rows of 16
         // bytes in groups of 2 KB (one 16-byte store per 16 bytes; key by key, single bytes would go to rows of
         // their own)
         {
@@ -614,13 +616,13 @@ __global__ void __launch_bounds__(128, CacheAttend<NH>::kPerSm) cache_attend_ker
             for (int h = 0; h < NH; h += 2) {
                 uint64_t rest = p[h / 2];
 #pragma unroll
-                for (int term = 0; term < 3; ++term) {
+                for (int term = 0; term < 4; ++term) {
                     float a, c;
                     f2_unpack(rest, a, c);
                     const uint16_t e = pack_e4m3x2(a, c);
                     w[(term * NH + h) / 4] |= static_cast<uint32_t>(e) << (h % 4 * 8);
                     // 16 (rest - e), exact
-                    if (term < 2) rest = ffma2(unpack_e4m3x2_f2(e), f2_pack(-16.f, -16.f), fmul2(rest, f2_pack(16.f, 16.f)));
+                    if (term < 3) rest = ffma2(unpack_e4m3x2_f2(e), f2_pack(-16.f, -16.f), fmul2(rest, f2_pack(16.f, 16.f)));
                 }
             }
 #pragma unroll
@@ -680,42 +682,32 @@ __global__ void __launch_bounds__(128, CacheAttend<NH>::kPerSm) cache_attend_ker
             const uint32_t row = tmem + SM::kTmemO + (static_cast<uint32_t>(warp * 32) << 16);
             const uint64_t sixteenth = f2_pack(0.0625f, 0.0625f);
             auto factor = [&](const float *f, int i) { return *reinterpret_cast<const uint64_t *>(f + 2 * i); };
-            auto add = [&](const float *t0, const float *t1, const float *t2) {
+            uint64_t acc[NH / 2];  // the terms so far, the smallest first
+            auto add = [&](const float *t, bool first) {
 #pragma unroll
                 for (int i = 0; i < NH / 2; ++i) {
-                    const uint64_t a = ffma2(f2_pack(t2[2 * i], t2[2 * i + 1]), sixteenth, f2_pack(t1[2 * i], t1[2 * i + 1]));
-                    o[i] = ffma2(ffma2(a, sixteenth, f2_pack(t0[2 * i], t0[2 * i + 1])), factor(head_new, i),
-                                 fmul2(o[i], factor(head_old, i)));
+                    const uint64_t x = f2_pack(t[2 * i], t[2 * i + 1]);
+                    acc[i] = first ? x : ffma2(acc[i], sixteenth, x);
                 }
             };
             if constexpr (NH == 4) {
                 float v[16];
                 tmem_ld16(row, v);
-                add(v, v + 4, v + 8);
-            } else if constexpr (NH == 8) {
-                float v[32];
-                tmem_ld32(row, v);
-                add(v, v + 8, v + 16);
-            } else if constexpr (NH == 16) {
-                float v[32], w[16];
-                tmem_ld32(row, v);
-                tmem_ld16(row + 32, w);
-                add(v, v + 16, w);
+#pragma unroll
+                for (int term = 3; term >= 0; --term) add(v + 4 * term, term == 3);
             } else {
-                uint64_t acc[16];
+                constexpr int kTerms = 32 / NH;  // of 32 columns
 #pragma unroll
-                for (int term = 2; term >= 0; --term) {
+                for (int part = 4 / kTerms - 1; part >= 0; --part) {
                     float v[32];
-                    tmem_ld32(row + 32 * term, v);
+                    tmem_ld32(row + 32 * part, v);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const uint64_t x = f2_pack(v[2 * i], v[2 * i + 1]);
-                        acc[i] = term == 2 ? x : ffma2(acc[i], sixteenth, x);
-                    }
+                    for (int term = kTerms - 1; term >= 0; --term)
+                        add(v + NH * term, part * kTerms + term == 3);
                 }
-#pragma unroll
-                for (int i = 0; i < 16; ++i) o[i] = ffma2(acc[i], factor(head_new, i), fmul2(o[i], factor(head_old, i)));
             }
+#pragma unroll
+            for (int i = 0; i < NH / 2; ++i) o[i] = ffma2(acc[i], factor(head_new, i), fmul2(o[i], factor(head_old, i)));
             tc_fence_before();
         }
         if (last) {
