@@ -73,10 +73,11 @@ __global__ void __launch_bounds__(append_threads(S), 1024 / append_threads(S)) c
     __shared__ float col[kRows][kCacheD];
     const int bh = blockIdx.x, b = bh / Hk, hk = bh % Hk;
     const int L = __ldg(cache_len + b), nn = n_new ? __ldg(n_new + b) : n;
-    if (L < 0 || nn < 0 || nn > n || nn > T - L) {  // nothing is written for this sequence
+    if (L < -1 || nn < 0 || nn > n || nn > T - L) {  // nothing is written for this sequence
         if (threadIdx.x == 0) record_error(ERR_CACHE_INPUT, 0x701);
         return;
     }
+    if (L < 0) return;  // an idle row
     const int j = L / S + blockIdx.y;
     const int64_t u0 = static_cast<int64_t>(j) * S;                      // the block's first token
     const int r0 = static_cast<int>(max(static_cast<int64_t>(L), u0) - u0);  // new rows [r0, r1)
@@ -214,11 +215,11 @@ __global__ void __launch_bounds__(128) cache_append_token_kernel(
     // the row does not depend on the length: both are asked for at once
     const uint4 v = __ldg(reinterpret_cast<const uint4 *>(X.p + b * X.st[0] + hk * X.st[1] + u * 8));
     const int L = __ldg(cache_len + b), nn = n_new ? __ldg(n_new + b) : 1;
-    if (L < 0 || nn < 0 || nn > 1 || nn > T - L) {
+    if (L < -1 || nn < 0 || nn > 1 || nn > T - L) {
         if (lane == 0) record_error(ERR_CACHE_INPUT, 0x704);
         return;
     }
-    if (nn == 0) return;
+    if (L < 0 || nn == 0) return;
     const int j = L / S, r0 = L % S;
     const size_t block = static_cast<size_t>(bh) * (T / S) + j;
     uint8_t *codes = (side ? V8 : K8) + block * S * kCacheD + u * 8;
@@ -317,8 +318,8 @@ __global__ void __launch_bounds__(kTopThreads) cache_evict_select_kernel(
     const int bh = blockIdx.x, b = bh / Hk, tid = threadIdx.x;
     int L = __ldg(cache_len + b);
     const int given = L;
-    if (L < 0 || L > T) {  // report; the sequence stays as it is
-        if (tid == 0) record_error(ERR_CACHE_INPUT, 0x702);
+    if (L < 0 || L > T) {  // the sequence stays as it is; -1 is an idle row, others are reported
+        if (L != -1 && tid == 0) record_error(ERR_CACHE_INPUT, 0x702);
         L = 0;
     }
     const int whole = L / s, begun = L % s > 0 ? 1 : 0;

@@ -192,7 +192,8 @@ class Cache8(NamedTuple):
 def cache_append(dims: L.Dims, cache: Cache8, cache_len: torch.Tensor, K: torch.Tensor, V: torch.Tensor,
                  n_new: Optional[torch.Tensor] = None) -> None:
     """Writes the tokens K, V [B, Hkv, n, d] (bf16, also strided views) at cache_len [B] (int32) of every sequence,
-    n_new[b] of them (default: n).  The caller advances cache_len, once for all layers."""
+    n_new[b] of them (default: n); cache_len[b] = -1 is an idle row, nothing of which is written.  The caller
+    advances cache_len, once for all layers."""
     dev = _device_of(K)
     B, Hk, _ = cache.check(dims, dev)
     if K.dim() != 4:

@@ -389,9 +389,10 @@ ssa_status_t ssa_rope_axes(const ssa_dims_t *dims, const int32_t *pos, int axes,
  * capacity in tokens, T % s == 0, T/s <= 8192, B*Hkv*T < 2^31; H any multiple of
  * Hkv.  cache_len [B] int32 (device) counts the tokens that come before those of
  * the call, as for ssa_sparse_decode: append at cache_len, decode at cache_len,
- * then the caller adds the new tokens, once for all layers.  Codes (and q, o,
- * Kbar) need 16-byte aligned base addresses.  Rows behind the last token may hold
- * anything; no call writes them.
+ * then the caller adds the new tokens, once for all layers.  cache_len[b] = -1 is
+ * an idle row of the batch in all three: its cache, weights and length stay as they
+ * are, and nothing is recorded.  Codes (and q, o, Kbar) need 16-byte aligned base
+ * addresses.  Rows behind the last token may hold anything; no call writes them.
  *
  * ssa_cache_append writes n_new[b] tokens of sequence b (NULL: n for all; 0
  * allowed) at positions cache_len[b] ..
@@ -405,7 +406,7 @@ ssa_status_t ssa_rope_axes(const ssa_dims_t *dims, const int32_t *pos, int axes,
  *              rounded again at the new scale.  Infinities and NaN are stored as NaN.
  *   Kbar       in/out, or NULL: row j is written when the call completes block j,
  *              with the mean of the keys as the cache holds them
- * A sequence with cache_len < 0, n_new outside [0, n] or more than T tokens in
+ * A sequence with cache_len < -1, n_new outside [0, n] or more than T tokens in
  * all records SSA_ERR_BAD_INPUT and keeps its cache as it was.
  */
 ssa_status_t ssa_cache_append(const ssa_dims_t *dims, int n, const int32_t *cache_len, const int32_t *n_new,
@@ -445,7 +446,7 @@ ssa_status_t ssa_cache_decode(const ssa_dims_t *dims, const int32_t *cache_len, 
  * the block begun behind them follows.  Tokens keep the rotary positions that their
  * keys were written with; the sequence's new length counts cache rows only.
  *   keep       1 .. T/s;  sink, recent >= 0, sink + recent <= keep
- *   cache_len  in  [B] int32, tokens that the cache holds, 0 .. T
+ *   cache_len  in  [B] int32, tokens that the cache holds, 0 .. T, or -1: an idle row
  *   new_len    out [B] int32 or NULL: keep * s + cache_len % s, or cache_len where
  *              nothing left; may be cache_len itself
  *   weight_in  in  [B, Hkv, T/s] fp32;  weight_out out or NULL: the weights in the
@@ -454,8 +455,8 @@ ssa_status_t ssa_cache_decode(const ssa_dims_t *dims, const int32_t *cache_len, 
  *   kept       out [B, Hkv, keep] int32: former indices of the complete blocks,
  *              ascending, -1 behind
  *   ws         >= ssa_workspace_size(dims, SSA_OP_CACHE_EVICT) bytes
- * A cache length outside [0, T] records SSA_ERR_BAD_INPUT; that sequence stays as it
- * was (kept = -1).
+ * An idle row stays as it was (kept = -1, new_len = -1, its weights unchanged); so does
+ * a sequence whose length is outside [-1, T], which records SSA_ERR_BAD_INPUT.
  */
 ssa_status_t ssa_cache_evict(const ssa_dims_t *dims, int keep, int sink, int recent, const int32_t *cache_len,
                              int32_t *new_len, const float *weight_in, float *weight_out, void *K8, float *Kscale,

@@ -8,7 +8,7 @@ from block_top_sparse_b200 import _lib as L
 from block_top_sparse_b200 import ops
 
 from . import cache_ref as R
-from .test_gpu_cache import D, filled, gen, i32
+from .test_gpu_cache import D, check_append, check_decode, filled, gen, i32, query, snapshot, unchanged
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -67,3 +67,54 @@ def test_decode_weights_hold_16_bits(s, G, place):
             tol = 2.0 ** -8 * np.abs(ro) + (2.0 ** -16 + 2 * e) * spread + 2 * 2.0 ** -30 * p.max(1, keepdims=True)
             off = np.abs(o[b, heads].double().cpu().numpy() - ro) / tol
             assert np.all(off <= 1.0), (b, h, np.max(off))
+
+
+@pytest.mark.parametrize("n,news", [(1, None), (1, [1, 1, 0, 1]), (100, None), (100, [100, 100, 0, 37])])
+@pytest.mark.parametrize("s", [64, 128])
+def test_idle_rows_are_idle_in_every_call(s, n, news):
+    """cache_len = -1 in a batch whose other rows work: one tensor of lengths serves append, decode and eviction; the
+    idle row keeps its cache, weights and length, whatever n_new says of it, and is no error."""
+    B, Hkv, T = 4, 2, 8 * s
+    dims = L.make_dims(B, 4, T, D, s, 0, Hkv=Hkv)
+    lens = [5 * s + 3, -1, -1, 4 * s - 1]
+    c = filled(dims, [T - 1] * B, seed=n)
+    cache_len = i32(*lens)
+    K, V = (torch.randn(B, Hkv, n, D, device="cuda", generator=gen(n + i)).bfloat16() for i in range(2))
+    n_new = None if news is None else i32(*news)
+    added = [0 if x < 0 else n if news is None else m for x, m in zip(lens, news or [n] * B)]
+    before = snapshot(c)
+    ops.cache_append(dims, c, cache_len, K, V, n_new)
+    assert L.ssa_get_device_error() == L.SSA_OK
+    assert unchanged(c, before, slice(1, 3))
+    check_append(dims, c, before, lens, added, K, V)
+
+    q, w = query(B, 4), torch.rand(B, Hkv, 8, device="cuda", generator=gen(3))
+    was = w.clone()
+    out = ops.cache_decode(dims, c, cache_len, q, weight_in=w, weight_out=w)
+    assert L.ssa_get_device_error() == L.SSA_OK
+    check_decode(dims, c, lens, q, out, was, w)
+
+    held = [x + m for x, m in zip(lens, added)]
+    before, was = snapshot(c), w.clone()
+    kept, new_len = ops.cache_evict(dims, c, i32(*held), 2, w, 1, 1, weight_out=w)
+    assert L.ssa_get_device_error() == L.SSA_OK
+    assert unchanged(c, before, slice(1, 3)) and torch.equal(w[1:3], was[1:3])
+    assert new_len.tolist() == [2 * s + held[0] % s, -1, -1, 2 * s + held[3] % s]
+    assert bool((kept[1:3] == -1).all()) and bool((kept[[0, 3]] >= 0).all())
+
+
+def test_lengths_below_idle_are_errors():
+    dims = L.make_dims(2, 2, 256, D, 64, 0)
+    c = filled(dims, [255] * 2)
+    before = snapshot(c)
+    for n in (1, 5):
+        K = torch.randn(2, 2, n, D, device="cuda", generator=gen(n)).bfloat16()
+        for lens in ([-2, -1], [-1, -2 ** 31]):
+            ops.cache_append(dims, c, i32(*lens), K, K)
+            assert L.ssa_get_device_error() == L.SSA_ERR_BAD_INPUT
+        ops.cache_append(dims, c, i32(-1, -1), K, K, i32(0, n + 1))  # a count out of range stays one
+        assert L.ssa_get_device_error() == L.SSA_ERR_BAD_INPUT
+    w = torch.rand(2, 2, 4, device="cuda", generator=gen(1))
+    _, new_len = ops.cache_evict(dims, c, i32(-2, -1), 1, w)
+    assert L.ssa_get_device_error() == L.SSA_ERR_BAD_INPUT
+    assert new_len.tolist() == [-2, -1] and unchanged(c, before)
