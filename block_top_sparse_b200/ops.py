@@ -155,7 +155,24 @@ def rope_axes(dims: L.Dims, pos: torch.Tensor, sections, Q: torch.Tensor, K: Opt
 
 class Cache8(NamedTuple):
     """An 8-bit key/value cache: codes [B, Hkv, T, d] (float8_e4m3fn), scales [B, Hkv, T/s] fp32 and, for sparse
-    decoding, the pooled keys [B, Hkv, T/s, d] fp32 (None: not kept)."""
+    decoding, the pooled keys [B, Hkv, T/s, d] fp32 (None: not kept).
+
+    Each layer has a cache (and weights), all share one tensor of lengths: cache_len[b] tokens held, -1 for an idle
+    row.  It changes between the layers' calls only.  A step with n_new[b] <= n new tokens per sequence (0 for idle
+    rows), where dims.T is the capacity, dims_n.T = n, and rows = arange(B)::
+
+        last = torch.where(n_new > 0, cache_len + n_new - 1, -1)   # position of the newest token, -1: none
+        at = (n_new - 1).clamp(min=0).long()                       # and its place among the n
+        for layer, cache, w in zip(layers, caches, weights):
+            q, k, v = layer(x)                                     # [B, H or Hkv, n, d], views of a projection
+            q, k = ops.rope_axes(dims_n, pos, sections, q, k)
+            ops.cache_append(dims, cache, cache_len, k, v, n_new)
+            o, lse, idx = ops.cache_decode(dims, cache, last, q[rows, :, at].contiguous(), weight_in=w, weight_out=w)
+        cache_len += n_new                                         # once, behind the last layer
+        for cache, w in zip(caches, weights):                      # each with the lengths from before
+            kept, new_len = ops.cache_evict(dims, cache, cache_len, keep, w, sink=sink, recent=recent, weight_out=w)
+        cache_len.copy_(new_len)                                   # the same for every layer
+    """
     K8: torch.Tensor
     Kscale: torch.Tensor
     V8: torch.Tensor
@@ -241,7 +258,9 @@ def cache_evict(dims: L.Dims, cache: Cache8, cache_len: torch.Tensor, keep: int,
                 ws: Optional[torch.Tensor] = None):
     """Keeps `keep` complete blocks of every sequence and key/value head: the first `sink`, the last `recent` and the
     ones of greatest weight [B, Hkv, T/s]; the cache is compacted in place.  weight_out (may be weight) receives the
-    weights in the new order, new_len (default: a new tensor; may be cache_len) the lengths.  Returns (kept, new_len)."""
+    weights in the new order, new_len (default: a new tensor) the lengths.  Every layer's call needs the lengths from
+    before, so new_len may be cache_len only where no other cache is still to be evicted by them.  Returns
+    (kept, new_len)."""
     dev = _device_of(weight)
     scales = cache.check(dims, dev)
     B, Hk, _ = scales

@@ -448,7 +448,11 @@ ssa_status_t ssa_cache_decode(const ssa_dims_t *dims, const int32_t *cache_len, 
  *   keep       1 .. T/s;  sink, recent >= 0, sink + recent <= keep
  *   cache_len  in  [B] int32, tokens that the cache holds, 0 .. T, or -1: an idle row
  *   new_len    out [B] int32 or NULL: keep * s + cache_len % s, or cache_len where
- *              nothing left; may be cache_len itself
+ *              nothing left.  The caches of several layers share their lengths, and
+ *              every layer's call reads those from before the eviction, so new_len may
+ *              be cache_len itself only where no other cache is evicted by it later (a
+ *              second layer given the shortened length would leave its newest blocks
+ *              behind it)
  *   weight_in  in  [B, Hkv, T/s] fp32;  weight_out out or NULL: the weights in the
  *              blocks' new order, 0 behind them; may be weight_in itself
  *   K8, Kscale, V8, Vscale, Kbar (or NULL)  in/out

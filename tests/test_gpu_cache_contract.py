@@ -8,7 +8,7 @@ from block_top_sparse_b200 import _lib as L
 from block_top_sparse_b200 import ops
 
 from . import cache_ref as R
-from .test_gpu_cache import D, check_append, check_decode, filled, gen, i32, query, snapshot, unchanged
+from .test_gpu_cache import D, check_append, check_decode, check_evict, filled, gen, i32, query, snapshot, unchanged
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -118,3 +118,68 @@ def test_lengths_below_idle_are_errors():
     _, new_len = ops.cache_evict(dims, c, i32(-2, -1), 1, w)
     assert L.ssa_get_device_error() == L.SSA_ERR_BAD_INPUT
     assert new_len.tolist() == [-2, -1] and unchanged(c, before)
+
+
+def test_the_documented_loop_with_several_layers():
+    """Three layers of a model share one tensor of lengths over a prompt, pieces, single tokens and idle rows, by the
+    loop of Cache8's documentation as it is written; every call against the definitions."""
+    from .test_cache_loop import documented_loop
+    B, H, Hkv, s, T, keep, layers = 4, 4, 2, 64, 512, 3, 3
+    dims = L.make_dims(B, H, T, D, s, 2, Hkv=Hkv)
+    caches = [filled(dims, [-1] * B, seed=i) for i in range(layers)]   # nothing held: all garbage
+    weights = [torch.zeros(B, Hkv, T // s, device="cuda") for _ in range(layers)]
+    g, cache_len = gen(5), i32(0, 0, -1, 0)
+    calls = []
+
+    class Checked:
+        rope_axes = staticmethod(ops.rope_axes)
+
+        @staticmethod
+        def cache_append(dims, c, cache_len, K, V, n_new):
+            before = snapshot(c)
+            ops.cache_append(dims, c, cache_len, K, V, n_new)
+            check_append(dims, c, before, cache_len.tolist(), n_new.tolist(), K, V)
+
+        @staticmethod
+        def cache_decode(dims, c, last, q, weight_in, weight_out):
+            was = weight_in.clone()
+            out = ops.cache_decode(dims, c, last, q, weight_in, weight_out)
+            check_decode(dims, c, last.tolist(), q, out, was, weight_out)
+            return out
+
+        @staticmethod
+        def cache_evict(dims, c, cache_len, keep, weight, sink, recent, weight_out):
+            before, was, lens = snapshot(c), weight.clone(), cache_len.tolist()
+            kept, new_len = ops.cache_evict(dims, c, cache_len, keep, weight, sink, recent, weight_out)
+            for b, n in enumerate(lens):
+                if n < 0:
+                    assert unchanged(c, before, slice(b, b + 1)) and int(new_len[b]) == -1
+            live = [b for b, n in enumerate(lens) if n >= 0]
+            if len(live) == len(lens):
+                check_evict(dims, c, before, lens, keep, sink, recent, was, kept, new_len, weight_out)
+            else:
+                sub = lambda t: t[live].contiguous()  # noqa: E731
+                check_evict(L.make_dims(len(live), H, T, D, s, 0, Hkv=Hkv),
+                            ops.Cache8(*(sub(t.view(torch.uint8)).view(t.dtype) for t in c)), [sub(t) for t in before],
+                            [lens[b] for b in live], keep, sink, recent, sub(was), kept[live], new_len[live], sub(weight_out))
+            calls.append(lens)
+            return kept, new_len
+
+    loop = documented_loop()
+    for step, news in enumerate([[300, 1, 0, 64], [40, 0, 0, 100], [1, 1, 0, 1], [7, 0, 0, 90], [1, 1, 0, 1], [1, 200, 1, 1]]):
+        if step == 5:
+            cache_len[2] = 0  # a sequence takes the idle row
+        n = max(news)
+        qkv = [torch.randn(B, n, H + 2 * Hkv, D, device="cuda", generator=g).bfloat16() for _ in range(layers)]
+        project = lambda x, i: tuple(t.transpose(1, 2) for t in qkv[i].split([H, Hkv, Hkv], 2))  # noqa: E731
+        env = dict(ops=Checked, torch=torch, dims=dims, dims_n=L.make_dims(B, H, n, D, s, 0, Hkv=Hkv), caches=caches,
+                   pos=torch.randint(0, 5000, (3, B, n), device="cuda", dtype=torch.int32, generator=g),
+                   sections=[16, 24, 24], layers=[lambda x, i=i: project(x, i) for i in range(layers)], x=None,
+                   weights=weights, cache_len=cache_len, n_new=i32(*news), rows=torch.arange(B, device="cuda"),
+                   keep=keep, sink=1, recent=1)
+        exec(loop, env)
+        lens = calls[-1]
+        assert calls[-layers:] == [lens] * layers
+        assert cache_len.tolist() == [n if n < 0 else min(n // s, keep) * s + n % s for n in lens]
+        assert L.ssa_get_device_error() == L.SSA_OK
+    assert max(map(max, calls)) > (keep + 1) * s and cache_len.tolist()[2] == 1  # blocks did leave
