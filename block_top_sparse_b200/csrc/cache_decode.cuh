@@ -524,13 +524,12 @@ __global__ void __launch_bounds__(128, CacheAttend<NH>::kPerSm) cache_attend_ker
 #pragma unroll
             for (int i = 0; i < NH / 2; ++i) {
                 p[i] = fmul2(p[i], fmul2(kk, *reinterpret_cast<const uint64_t *>(head_f + 2 * i)));
-                float a, c, ma, mc;
+                float a, c;
                 f2_unpack(p[i], a, c);
                 a = valid ? a : -INFINITY;
                 c = valid ? c : -INFINITY;
                 p[i] = f2_pack(a, c);
-                asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(ma) : "f"(a));
-                asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(mc) : "f"(c));
+                const float ma = warp_max(a), mc = warp_max(c);
                 mine = lane == 2 * i ? ma : lane == 2 * i + 1 ? mc : mine;
             }
             if (lane < NH) atomic_max_shared(now_m + tid / S * NH + lane, mine);

@@ -518,6 +518,14 @@ __device__ __forceinline__ uint64_t unpack_e4m3x2_f2(uint16_t v) {
     return f2_pack(f.x, f.y);
 }
 
+// Largest value over the warp, NaN apart.  Volatile: all 32 lanes must take part, so it must not move into a branch
+// around its use.
+__device__ __forceinline__ float warp_max(float v) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+
 // Raises a float in shared memory to v, in whatever order several threads come: as integers, floats >= 0 grow
 // with their value and negative ones fall (+ 0.f: -0 counts as 0).
 __device__ __forceinline__ void atomic_max_shared(float *to, float v) {
