@@ -226,19 +226,15 @@ __global__ void __launch_bounds__(128) cache_append_token_kernel(
     float *scale = (side ? Vscale : Kscale) + block;
     const float old = r0 > 0 ? *scale : 0.f;
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t top = 0, finite = 0;
+    uint32_t finite = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint32_t lo = w[i] & 0x7FFFu, hi = (w[i] >> 16) & 0x7FFFu;
-        top = max(top, max(lo, hi));
         if (lo < 0x7F80u) finite = max(finite, lo);
         if (hi < 0x7F80u) finite = max(finite, hi);
     }
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) {
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-        finite = max(finite, __shfl_xor_sync(0xffffffffu, finite, o));
-    }
+    for (int o = 8; o > 0; o >>= 1) finite = max(finite, __shfl_xor_sync(0xffffffffu, finite, o));
     const float want = fmaxf(e4m3_scale(__uint_as_float(finite << 16)), old), inv = pow2_inverse(want);
     if (r0 > 0 && want > old) {  // the older rows move to the larger scale
         const float ratio = old * inv;
@@ -260,7 +256,7 @@ __global__ void __launch_bounds__(128) cache_append_token_kernel(
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         float lo = __uint_as_float(w[i] << 16) * inv, hi = __uint_as_float(w[i] & 0xFFFF0000u) * inv;
-        if (top >= 0x7F80u) lo = (lo - lo) + lo, hi = (hi - hi) + hi;  // infinity -> NaN
+        lo = fabsf(lo) < INFINITY ? lo : NAN, hi = fabsf(hi) < INFINITY ? hi : NAN;  // (-0 stays -0)
         c[i] = pack_e4m3x2(lo, hi);
     }
     *reinterpret_cast<uint2 *>(codes + r0 * kCacheD) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);

@@ -183,3 +183,18 @@ def test_the_documented_loop_with_several_layers():
         assert cache_len.tolist() == [n if n < 0 else min(n // s, keep) * s + n % s for n in lens]
         assert L.ssa_get_device_error() == L.SSA_OK
     assert max(map(max, calls)) > (keep + 1) * s and cache_len.tolist()[2] == 1  # blocks did leave
+
+
+@pytest.mark.parametrize("n", [1, 3])
+def test_append_keeps_the_sign_of_zero_beside_an_infinity(n):
+    """The code of -0 is 0x80 whatever stands beside it, in the single-token form as in the other."""
+    dims = L.make_dims(1, 2, 128, D, 64, 0)
+    K = torch.zeros(1, 2, n, D, dtype=torch.bfloat16, device="cuda")
+    K[..., 1::2] = -0.0
+    K[0, 0, 0, 0], K[0, 0, 0, 2], K[0, 0, 0, 3] = float("inf"), float("-inf"), float("nan")
+    for at in (0, 63):
+        c = filled(dims, [at - 1])
+        before = snapshot(c)
+        ops.cache_append(dims, c, i32(at), K, K)
+        assert L.ssa_get_device_error() == L.SSA_OK
+        check_append(dims, c, before, [at], [n], K, K)
