@@ -198,3 +198,27 @@ def test_append_keeps_the_sign_of_zero_beside_an_infinity(n):
         ops.cache_append(dims, c, i32(at), K, K)
         assert L.ssa_get_device_error() == L.SSA_OK
         check_append(dims, c, before, [at], [n], K, K)
+
+
+def test_rows_off_a_16_byte_boundary_are_refused():
+    """Views of the right shape whose strides fit but whose base does not: the library refuses them, by its status."""
+    dims = L.make_dims(1, 4, 256, D, 64, 0)
+    c = filled(dims, [9])
+    before = snapshot(c)
+    wide = torch.zeros(1, 4, 30, D + 8, dtype=torch.bfloat16, device="cuda")
+    odd, even = wide[..., 1:1 + D], wide[..., 8:]
+    assert odd.shape == even.shape and odd.stride() == even.stride() and odd.data_ptr() % 16 == 2
+    for K, V in ((odd, even), (even, odd)):
+        with pytest.raises(L.SSAError):
+            ops.cache_append(dims, c, i32(10), K, V)
+    assert unchanged(c, before)
+    rope = L.make_dims(1, 4, 30, D, 64, 0)
+    pos = torch.zeros(1, 1, 30, dtype=torch.int32, device="cuda")
+    for args in ((odd,), (even, odd)):
+        with pytest.raises(L.SSAError):
+            ops.rope_axes(rope, pos, [64], *args)
+    with pytest.raises(L.SSAError):
+        ops.rope_axes(rope, pos, [64], even, out=(odd, None))
+    ops.cache_append(dims, c, i32(10), even, even)      # the same view on its boundary is taken
+    assert torch.equal(ops.rope_axes(rope, pos, [64], even)[0], even)
+    assert L.ssa_get_device_error() == L.SSA_OK
