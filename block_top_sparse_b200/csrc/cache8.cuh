@@ -59,8 +59,9 @@ struct CacheRows {
 
 // grid (B * Hk, blocks that n rows can touch, 2: keys, values): 16 threads of 8 elements per row, kAppendPasses
 // passes over the block's rows, all of them in flight at once.  (A 32K prompt of 8 heads, blocks of 128, and
-// ragged pieces of 16 heads, blocks of 64: 37 and 14.7 us; with 4 passes by twice the threads 52 and 17.2 us,
-// with 16 by half of them 37 and 17.8 us.)
+// ragged pieces of 16 heads, blocks of 64, in a captured graph: 33.6 and 13.7 us; with 4 passes by twice the threads
+// 46.4 and 17.0 us, with 16 by half of them 49.0 and 20.0 us.  The launch bounds keep 1024 threads on an SM at 64
+// registers, 40 and 52 bytes of which spill; at 512 threads and 96 registers nothing does: 43.9 and 15.1 us.)
 constexpr int kAppendPasses = 8;
 constexpr int append_threads(int s) { return 16 * s / kAppendPasses; }
 
@@ -203,7 +204,10 @@ __global__ void __launch_bounds__(append_threads(S), 1024 / append_threads(S)) c
 
 // One new token per sequence (n = 1): a warp per (sequence, key head), lanes 0-15 the key, lanes 16-31 the
 // value, no barrier; grid ceil(B * Hk / 4).  The decode step's form: its time is that of the loads after one
-// another (length, row and scale, store); 64 sequences, 8 key heads: 2.2 us, 6.2 us with a CTA per block.
+// another (length, row and scale, store); kernel time for 64 sequences, 8 key heads: 2.1 us, 6.2 us with a CTA per
+// block.  A step in which some token outgrows its block's scale, as most steps of a batch of this size have one, waits for
+// the older rows of that block to be moved, eight per round trip: 4 us more with 43 older rows, 10 us more with 126; a
+// step that completes every block 3 us more.
 template <int S>
 __global__ void __launch_bounds__(128) cache_append_token_kernel(
     const int32_t *__restrict__ cache_len, const int32_t *__restrict__ n_new, const CacheRows K, const CacheRows V,

@@ -17,8 +17,8 @@
 //                                  head's largest element,
 //   p = (t0 + t1/16 + t2/256 + t3/4096)/256: 16 bits, error <= 2^-16 p (four roundings,
 //                                  each at most 2^-4 of what is left) + 2^-30 of a tile's largest.
-// (Three terms, 12 bits, showed where values cancel: with weights 2^-10 apart, what is left was off by up to
-// 2^-2.6 of itself, now by 2^-8 with its rounding to bf16.)
+// (Three terms, 12 bits, showed where values cancel: of two weights 2^-10 apart, the difference was off by up to 9 %,
+// with four by 0.24 %, less than its rounding to bf16.)
 // The terms are extra columns (N) of the same product, and its results are put
 // together in fp32; N is small and the tensor cores have time to spare.
 //
@@ -246,8 +246,10 @@ struct CacheAttend {
     static constexpr int kTmemO = kApart ? kNS : 0;                  // first column of the output's product
     static constexpr int kCols = kTmemO + kNP;
     static constexpr int kTmemCols = kCols <= 32 ? 32 : kCols <= 64 ? 64 : 128;
-    // CTAs per SM.  64 caches of 16K to 32K tokens, 8 key heads, G = 4: 459 us with three, 458 us with four, 473 us
-    // with five; 16 ragged ones, G = 8, blocks of 64: 45, 35 and 35 us.  NH = 32 has registers for three.
+    // CTAs per SM.  64 caches of 16K to 32K tokens, 8 key heads, G = 4: 461 us with three, 453 us with four, 475 us
+    // with five; 16 ragged ones, G = 8, blocks of 64: 45, 35 and 35 us.  NH = 32, 64 caches of 8K to 16K tokens, one key
+    // head, blocks of 128 and 64: 75 and 86 us with three (168 registers, 124 and 164 bytes spilled), 78 and 94 us with
+    // two (nothing spilled).
     static constexpr int kPerSm = NH <= 16 ? 4 : 3;
 };
 
@@ -738,9 +740,17 @@ __global__ void __launch_bounds__(128, CacheAttend<NH>::kPerSm) cache_attend_ker
 // CTAs; the attention weight of the blocks from their own maxima and sums.  Where there are many pairs of few
 // partials a CTA takes eight heads of a pair, a warp each, then its share of the pair's blocks (SPLIT = 0).  Where a pair is
 // split over many CTAs, the first head_ctas CTAs take one head (SPLIT = 1) or a quarter of one head's dims (4)
-// each, and every CTA after them 256 blocks of one pair: 16 sequences of up to 32K tokens, 2 key heads, about
-// 23 partials a pair: 38 us in all with 1 and 43 us with 4; one of 131072 tokens, 1 key head, 592 partials: 27 us
-// and 18 us.
+// each, and every CTA after them 256 blocks of one pair.  The whole call for B caches of 16K to 32K tokens, one key
+// head, in a captured graph (us; 592 / B partials a pair), by form:
+//   partials a pair       8     12     16     20     33     49     66     99    148
+//   G = 4, form 0       77.7   57.7   47.1   42.2   35.4   34.7   36.8   40.8   55.3
+//          form 1       76.1   54.9   42.6   36.5   25.8   20.9   18.4   15.8   14.0
+//          form 4       84.5   59.8   46.4   38.9   25.7   20.4   17.0   13.9   12.3
+//   G = 16, form 0      81.0   61.4   51.2   45.4   38.2   38.3   40.8   46.3   59.2
+//           form 1      88.0   62.4   49.8   42.0   28.8   23.9   21.6   19.0   16.4
+//           form 4     120.3   82.5   63.5   52.4   34.6   26.5   23.0   17.8   15.4
+// Hence 1 from 16 partials a pair on and 4 from 64 on.  (At G = 16 form 1 is still ahead at 66, with block weights by
+// 25.6 to 28.8 us, and there by 21.0 to 21.4 us at 148.)
 // ---------------------------------------------------------------------------
 struct CachePartials {
     int n;

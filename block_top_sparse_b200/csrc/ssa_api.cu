@@ -1003,8 +1003,10 @@ ssa_status_t ssa_cache_decode(const ssa_dims_t *dims, const int32_t *cache_len, 
     CUtensorMap tmK, tmV;
     if (!make_tmap_codes(&tmK, K8, S.krows, S.s) || !make_tmap_codes(&tmV, V8, S.krows, S.s)) return SSA_ERR_CUDA;
     if (S.k > 0) {
-        // CTAs per pair: a second one only from 128 blocks on (each scores 64 at a time), while SMs are idle: one
-        // sequence of 131072 tokens, 8 key heads, 32 blocks of 128: 25 us in all with one CTA per pair, 19 us with eight
+        // CTAs per pair: a second one only from 128 blocks on (each scores 64 at a time), while SMs are idle.  The whole
+        // call, k = 16, s = 128, G = 4, with 1, 2, 4 and 8 (us): 1024 blocks, 8 pairs 28.1, 22.8, 20.5, 18.7 and 37
+        // pairs 34.1, 27.9, 23.9, 22.8; 256 blocks, 37 pairs 18.0, 17.2, 16.4, 17.1, 74 pairs 23.7, 22.5, 22.4, 24.6
+        // and 512 pairs 67.5, 70.5, 76.9, 90.4; 128 blocks, 74 pairs 21.0, 21.0, 21.1, 23.4
         unsigned parts = 1;
         while (parts < 8 && parts * 2 * bhk <= 2u * kCacheSms && static_cast<unsigned>(S.nb) >= 128 * parts) parts *= 2;
         cudaLaunchAttribute attr[1];

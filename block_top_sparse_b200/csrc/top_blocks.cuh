@@ -113,8 +113,8 @@ __device__ __forceinline__ void top_ascending(const uint32_t *keys, int n, int k
 // The same for n < 1024 by one warp, the keys in its registers (KPL per lane, n <= 32 * KPL): the kk-th
 // largest key is found two bits at a time from the first bit in which the keys differ (three candidates'
 // counts, 11 bits each, in one warp sum), stopping early at a candidate with exactly kk keys at or above it.
-// No barrier.  (Eviction of one of 17 blocks 7.7 us in all, selection of 16 of up to 256 blocks in 512 rows
-// 15.6 us; with the CTA's counts 9.0 and 16.4 us.)
+// No barrier.  (Calls in a captured graph: eviction of one of 17 blocks 7.6 us, sparse decode of 64 caches with 16 of
+// up to 256 blocks 66.2 us, of 64 caches with 16 of up to 128 40.5 us; with the CTA's counts 9.1, 66.7 and 41.6 us.)
 template <int KPL>
 __device__ __forceinline__ void top_ascending_warp(const uint32_t *keys, int n, int kk, int32_t *out, int lane) {
     uint32_t key[KPL], hi = 0u, lo = 0xFFFFFFFFu;
